@@ -1,6 +1,7 @@
 /*
  * qvae.h -- C ABI of libqvae: the W8A8 CausalConv3d layer of the Qwen-Image /
- * Wan VAE decoder on NVIDIA B200 (sm_100a).
+ * Wan VAE decoder, and 8-bit floating-point linear layers, on NVIDIA B200
+ * (sm_100a).
  *
  * The method (ComfyUI-Qwen-VAE-Triton v0.2.0 release note, sd114.wiki):
  *   - opening paragraph: an implicit-GEMM W8A8 kernel for the decoder's
@@ -23,7 +24,7 @@
  *   - Return value: QVAE_OK or a qvae_status code.  Argument errors are
  *     detected before anything is launched.  A device-side wait that ran out
  *     of time is reported later by qvae_get_error().
- *   - Layer geometry is fixed: 3x3x3 kernel, stride 1, causal temporal
+ *   - Convolution geometry is fixed: 3x3x3 kernel, stride 1, causal temporal
  *     padding of 2 leading zero frames, spatial padding 1 ("same" size).
  *     The streamed-chunk variant takes two carried frames in place of the
  *     zero frames, the row-band variant halo rows in place of the top and
@@ -348,6 +349,120 @@ size_t qvae_decode_workspace_bytes(const qvae_layer* layers, int32_t n);
  */
 int qvae_decode_layers(const qvae_layer* layers, int32_t n, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* ----------------------------- 8-bit floating-point linear layers -- */
+
+/*
+ * Linear layers in e4m3 with one scale for each block of 128, single or
+ * grouped by expert: the projections and feed-forward layers of the
+ * transformers whose latents the decoder above takes.  (The release note has
+ * no counterpart; the scheme is the decoder's -- weights quantised once,
+ * activations on the fly, products on the 8-bit tensor cores, bf16 in and out
+ * -- with floating-point codes and scales taken over 128 channels instead of a
+ * tensor.)
+ *   Group.  Activations: 128 consecutive input channels of one row.  Weights:
+ *   128 output x 128 input channels.  The last group of a row or matrix holds
+ *   what is left of it.
+ *   Scale.  2^e, e the least integer >= -126 with amax <= 448 * 2^e, held as
+ *   the byte e + 127 (E8M0).
+ *   Codes.  e4m3 of v * 2^-e, round half to even (the scaling is exact).
+ *   A group with an infinity or NaN has scale byte 255 and NaN codes: every
+ *   output that meets it is NaN.
+ *   out[m,n] = bf16_rne( sum over the blocks b of K of 2^(ex[m,b] + ew[n/128,b])
+ *              * sum over k in b of cx[m,k] * cw[n,k], + bias[n] ),
+ *   products exact, sums in fp32 on the tensor cores.
+ * M, N and K are any numbers from 1 on (M = 0 does nothing), N and K up to
+ * 2^20, M up to 2^30, E up to 1024, and E * ceil(N/128) * ceil(K/128) < 2^24;
+ * QVAE_ERR_SHAPE otherwise.  Rows of x and out may be `ldx`, `ldo` elements apart
+ * (rows of a wider buffer).  bf16 tensors (x, out, bias, w) may start at any
+ * element here; rows that all start on 16 bytes are read and written faster.
+ * Codes, scales and workspaces are 16-byte aligned.  out must not overlap what
+ * a call reads.  Unlike the convolution, no call restricts what may be
+ * launched right before it.  Needs nothing of earlier calls; calls on
+ * different streams are independent as long as their buffers are.
+ */
+
+/* What a layer quantises of its bf16 rows. */
+typedef enum qvae_fp8_op {
+  QVAE_FP8_PLAIN = 0,    /* x[m,k], rows of K */
+  QVAE_FP8_SILU_MUL = 1  /* g / (1 + exp(-g)) * u in fp32, g = x[m,k], u = x[m,K+k]: rows of 2 K ([gate | up]) */
+} qvae_fp8_op;
+
+/* Bytes of the packed codes (E * ceil(N/128) * ceil(K/128) tiles of 16 KiB) and of the scales
+ * (E * ceil(N/128) * ceil(K/512) words) of E weight matrices [N][K]; 0 for sizes out of range. */
+size_t qvae_fp8_packed_weight_bytes(int32_t E, int32_t N, int32_t K);
+size_t qvae_fp8_weight_scale_bytes(int32_t E, int32_t N, int32_t K);
+
+/*
+ * One-time weight quantisation and repack.
+ *   w_bf16     [E][N][K] bf16 (E = 1 for a single layer).
+ *   wq_packed  written: codes in the product's order, [e][n / 128][k / 128]
+ *              tiles of 128 rows x 128 bytes, the 16-byte group g of row r at
+ *              position g ^ (r % 8), zeros beyond N and K.
+ *   w_scale    written: scale bytes [e][n / 128][4 * ceil(K / 512)], byte b of
+ *              a row being block b of K; bytes beyond the last block are 1.
+ */
+int qvae_fp8_quantize_weights(int32_t E, int32_t N, int32_t K, const void* w_bf16, uint8_t* wq_packed,
+                              uint8_t* w_scale, void* stream);
+
+/* Bytes of the codes (M rows of 128 * ceil(K/128)) and scales (M * ceil(K/512) words) of M rows,
+ * and of a workspace that holds both (the _fused entry points); 0 for sizes out of range. */
+size_t qvae_fp8_code_bytes(int64_t M, int32_t K);
+size_t qvae_fp8_scale_bytes(int64_t M, int32_t K);
+size_t qvae_fp8_workspace_bytes(int64_t M, int32_t K);
+
+/*
+ * Dynamic activation quantisation of M rows.
+ *   op        qvae_fp8_op: what is quantised.
+ *   x_bf16    rows of K (QVAE_FP8_SILU_MUL: 2 K) bf16 values, ldx elements apart.
+ *   xq        [M][128 * ceil(K/128)] codes, written; zeros beyond K.
+ *   x_scale   [ceil(K/512)][M] words, written: byte j of word (g, m) is the
+ *             scale of row m's block 4 g + j (1 beyond the last block).
+ */
+int qvae_fp8_quant_act(int64_t M, int32_t K, int32_t op, const void* x_bf16, int64_t ldx, uint8_t* xq,
+                       uint32_t* x_scale, void* stream);
+
+/*
+ * The product of quantised rows with one weight matrix.
+ *   xq, x_scale          from qvae_fp8_quant_act.
+ *   wq_packed, w_scale   from qvae_fp8_quantize_weights with E = 1.
+ *   bias_bf16            [N] bf16 or NULL.
+ *   out_bf16             M rows of N bf16, ldo elements apart, written (columns
+ *                        from N on are left as they are).
+ */
+int qvae_linear_fp8(int64_t M, int32_t N, int32_t K, const uint8_t* xq, const uint32_t* x_scale,
+                    const uint8_t* wq_packed, const uint8_t* w_scale, const void* bias_bf16, void* out_bf16,
+                    int64_t ldo, void* stream);
+
+/*
+ * The products of rows sorted by expert with their experts' matrices: rows
+ * offsets[e] .. offsets[e + 1] - 1 meet matrix e (and bias row e).
+ *   offsets   [E + 1] int32 on the DEVICE, not decreasing, 0 <= . <= M; an expert
+ *             without rows costs nothing.  Rows before offsets[0] and from
+ *             offsets[E] on are left as they are.  (Values outside 0..M are
+ *             clipped and a span that would end before it starts is empty: no
+ *             access leaves the M rows.)
+ *   wq_packed, w_scale   from qvae_fp8_quantize_weights with this E.
+ *   bias_bf16 [E][N] or NULL.
+ */
+int qvae_linear_fp8_grouped(int32_t E, int64_t M, int32_t N, int32_t K, const uint8_t* xq, const uint32_t* x_scale,
+                            const int32_t* offsets, const uint8_t* wq_packed, const uint8_t* w_scale,
+                            const void* bias_bf16, void* out_bf16, int64_t ldo, void* stream);
+
+/*
+ * The whole layer from its bf16 rows: qvae_fp8_quant_act, then the product,
+ * with the same outputs.
+ *   op, x_bf16, ldx   as in qvae_fp8_quant_act.
+ *   workspace         qvae_fp8_workspace_bytes(M, K) bytes of scratch; calls
+ *                     that may overlap need one each.
+ */
+int qvae_linear_fp8_fused(int64_t M, int32_t N, int32_t K, int32_t op, const void* x_bf16, int64_t ldx,
+                          const uint8_t* wq_packed, const uint8_t* w_scale, const void* bias_bf16, void* out_bf16,
+                          int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+int qvae_linear_fp8_grouped_fused(int32_t E, int64_t M, int32_t N, int32_t K, int32_t op, const void* x_bf16,
+                                  int64_t ldx, const int32_t* offsets, const uint8_t* wq_packed,
+                                  const uint8_t* w_scale, const void* bias_bf16, void* out_bf16, int64_t ldo,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /* -------------------------------------------------------------- control -- */
 

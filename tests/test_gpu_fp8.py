@@ -1,0 +1,482 @@
+"""The 8-bit floating-point linear layers on the GPU against 64-bit arithmetic.
+
+Codes and scales are exact (compared bit for bit).  Products are compared with
+the 64-bit product of what the codes stand for, within the tolerance that
+fp8_reference derives from the arithmetic.
+"""
+import os
+import sys
+
+import pytest
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import fp8_reference as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from video_vae_decode_b200 import qvae
+    qvae.lib()
+    return qvae
+
+
+def rows(m, k, seed, extra=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((m, k + extra), generator=g) * torch.exp(torch.randn((m, 1), generator=g))
+    x = x * torch.where(torch.rand((1, k + extra), generator=g) < 0.02, 20.0, 1.0)
+    return x.to(torch.bfloat16).cuda()[:, :k]
+
+
+def matrix(shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * torch.exp(torch.randn(shape[:-1] + (1,), generator=g) * 0.5)
+            * shape[-1] ** -0.5).to(torch.bfloat16).cuda()
+
+
+def code_bits(values):
+    """e4m3 bytes of exact code values (float64), every NaN as 0x7F, zeros without sign."""
+    b = values.float().to(torch.float8_e4m3fn).view(torch.uint8)
+    b = torch.where(torch.isnan(values), torch.full_like(b, 0x7F), b)
+    return torch.where(b == 0x80, torch.zeros_like(b), b)
+
+
+def plain_bits(codes):
+    b = torch.where((codes & 0x7F) == 0x7F, torch.full_like(codes, 0x7F), codes)
+    return torch.where(b == 0x80, torch.zeros_like(b), b)
+
+
+def scale_bytes(words, kb):
+    """[M, kb] bytes of scale words [kg, M]."""
+    m = words.shape[1]
+    return words.contiguous().view(torch.uint8).view(words.shape[0], m, 4).permute(1, 0, 2).reshape(m, -1)[:, :kb]
+
+
+def unpack(w):
+    """(codes [E, 128 nblk, 128 Kb], scale bytes [E, nblk, Kb]) of packed weights, undoing tiles and swizzle."""
+    nblk, kb, kg = -(-w.N // 128), -(-w.K // 128), -(-w.K // 512)
+    t = w.wq.view(w.E, nblk, kb, 128, 8, 16)
+    r = torch.arange(128, device=t.device)
+    g = torch.arange(8, device=t.device)
+    t = t[:, :, :, r[:, None], g[None, :] ^ (r[:, None] % 8)]
+    return (t.permute(0, 1, 3, 2, 4, 5).reshape(w.E, nblk * 128, kb * 128),
+            w.w_scale.view(w.E, nblk, kg * 4)[:, :, :kb], w.w_scale.view(w.E, nblk, kg * 4)[:, :, kb:])
+
+
+def check_product(out, y, s, K):
+    err = (out.double() - y).abs()
+    tol = ref.tolerance(y, s, K)
+    bad = ~(err <= tol)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outputs off, worst {float((err / tol.clamp(min=1e-300)).max())} of the tolerance"
+
+
+# ------------------------------------------------------------- quantisers
+
+@pytest.mark.parametrize("m,k,extra", [(1, 1, 0), (1, 128, 0), (3, 127, 0), (5, 130, 0), (33, 512, 8), (31, 520, 3),
+                                       (70, 1000, 24), (257, 1176, 0), (2, 8192, 0), (1030, 96, 32)])
+def test_activation_codes_and_scales_are_exact(q, m, k, extra):
+    x = rows(m, k, m * 7 + k, extra)
+    x[:, :1] *= 0.0                                       # zeros among the values
+    if m > 2:
+        x[1] = 0.0                                        # a row of zeros
+        x[2] *= 2.0 ** -120                               # and one of tiny values
+    codes, words = q.fp8_quant_act(x)
+    want, byte = ref.quantise(x, 1)
+    assert torch.equal(scale_bytes(words, byte.shape[1]).long(), byte)
+    assert torch.equal(plain_bits(codes), code_bits(want))
+    assert (scale_bytes(words, words.shape[0] * 4)[:, byte.shape[1]:] == 1).all()
+    assert q.qvae_get_error() == 0
+
+
+def test_activation_codes_of_every_bf16_value(q):
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    x = bits.view(torch.bfloat16).cuda()
+    x = torch.where(torch.isfinite(x.float()), x, torch.zeros_like(x)).view(512, 128)
+    for y in (x, x.flatten()[torch.randperm(65536, generator=torch.Generator().manual_seed(1)).cuda()].view(64, 1024)):
+        codes, words = q.fp8_quant_act(y.contiguous())
+        want, byte = ref.quantise(y, 1)
+        assert torch.equal(scale_bytes(words, byte.shape[1]).long(), byte)
+        assert torch.equal(plain_bits(codes), code_bits(want))
+
+
+def test_activation_groups_with_infinities_and_nan(q):
+    x = rows(6, 300, 3)
+    x[1, 5], x[2, 130], x[3, 299] = float("inf"), float("nan"), float("-inf")
+    codes, words = q.fp8_quant_act(x)
+    want, byte = ref.quantise(x, 1)
+    assert (byte == 255).sum() == 3
+    assert torch.equal(scale_bytes(words, 3).long(), byte)
+    # the group's codes are NaN, the padding of its last block included
+    assert torch.equal(plain_bits(codes), code_bits(want))
+
+
+@pytest.mark.parametrize("m,k,extra", [(1, 1, 0), (4, 129, 0), (65, 1024, 16), (9, 1000, 0), (40, 333, 5)])
+def test_activation_codes_of_silu_mul(q, m, k, extra):
+    h = rows(m, 2 * k, m + k, extra)
+    if m > 2:
+        h[1, :k] = -100.0                                 # exp(-gate) beyond fp32
+        h[2, :k] = 90.0
+    codes, words = q.fp8_quant_act(h, silu_mul=True)
+    v = ref.silu_mul(h)
+    # computed in fp32: a value next to a border of the codes may take either neighbour.  exp, the sum, the
+    # divide and the product are off by at most (|gate| + 4) 2^-22 of the value; half a step of the code more
+    amax = ref.blocks(v, 1).abs().amax(3).amax(1)
+    byte = scale_bytes(words, amax.shape[1]).long()
+    rel = (h[:, :k].double().abs() + 4) * 2.0 ** -22
+    scale = torch.exp2(byte.double() - 127)
+    assert ((amax * (1 - 2.0 ** -14) <= 448 * scale) & ((byte == 1) | (amax * (1 + 2.0 ** -14) > 224 * scale))).all()
+    got = codes.view(torch.float8_e4m3fn).double().view(m, -1, 128) * scale[:, :, None]
+    got = got.view(m, -1)
+    assert (got[:, k:] == 0).all()
+    s = scale.repeat_interleave(128, 1)[:, :k]
+    half = torch.exp2(torch.floor(torch.log2(torch.clamp(v.abs() / s, min=2.0 ** -6))) - 4) * s
+    # a value below a power of two may be rounded on the finer or the coarser side of it.  Where exp(-gate) is beyond
+    # fp32 (gate < -88.72 = ln 2^-128) the fp32 form gives 0; what it should give is at most
+    # |gate| exp(gate) |up| <= 88.72 * 2^-128 |up| < 2^-121 |up| there (x exp(-x) falls for x > 1)
+    lost = torch.where(h[:, :k] < -88.5, 2.0 ** -121, 0.0) * h[:, k:2 * k].double().abs()
+    assert bool(((got[:, :k] - v).abs() <= half * (1 + 2.0 ** -8) + rel * v.abs() + 2.0 ** -149 + lost).all())
+
+
+@pytest.mark.parametrize("e,n,k", [(1, 1, 1), (1, 128, 128), (2, 130, 200), (1, 1000, 1176), (3, 64, 515), (1, 257, 127)])
+def test_packed_weights_are_exact(q, e, n, k):
+    w = matrix((e, n, k), e + n + k)
+    w[0, 0] *= 2.0 ** 30
+    if n > 128:
+        w[-1, 128:] = 0.0
+    p = q.fp8_quantize_weights(w if e > 1 else w[0])
+    assert (p.E, p.N, p.K) == (e, n, k)
+    codes, byte, pads = unpack(p)
+    assert (pads == 1).all()
+    for i in range(e):
+        want, wb = ref.quantise(w[i], 128)
+        assert torch.equal(byte[i].long(), wb)
+        assert torch.equal(plain_bits(codes[i]), code_bits(want))
+
+
+# --------------------------------------------------------------- products
+
+SIZES = [(1, 1, 1), (1, 128, 128), (1, 2048, 2048), (2, 130, 96), (7, 1000, 1176), (16, 512, 4096), (17, 384, 640),
+         (33, 257, 511), (64, 64, 8192), (77, 1000, 1176), (100, 96, 33), (128, 128, 513), (129, 200, 384), (200, 640, 129),
+         (240, 256, 256), (241, 384, 256), (300, 1024, 1024), (512, 512, 512), (999, 330, 700), (1500, 1152, 64),
+         (4097, 136, 160)]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES, ids=lambda v: str(v))
+@pytest.mark.parametrize("bias", [False, True])
+def test_linear_matches_the_exact_product(q, m, n, k, bias):
+    x, w = rows(m, k, m + n + k), matrix((n, k), m + 2 * n)
+    b = matrix((1, n), 5)[0] * 8 if bias else None
+    p = q.fp8_quantize_weights(w)
+    out = q.linear_fp8(*q.fp8_quant_act(x), p, b)
+    assert q.qvae_get_error() == 0
+    y, s = ref.linear(ref.act_values(x), ref.weight_values(w), b)
+    check_product(out, y, s, k)
+    again = q.linear_fp8_fused(x, p, b)
+    assert q.qvae_get_error() == 0
+    check_product(again, y, s, k)
+
+
+def test_scales_of_every_block_reach_their_products(q):
+    # one block's scale differs by a lot from the others': a wrong byte or row cannot hide
+    m, n, k = 150, 400, 1300
+    x, w = rows(m, k, 1), matrix((n, k), 2)
+    g = torch.Generator().manual_seed(3)
+    for r in range(m):
+        for b in range(11):
+            x[r, b * 128:(b + 1) * 128] *= 2.0 ** int(torch.randint(-12, 13, (1,), generator=g))
+    for i in range(4):
+        for b in range(11):
+            w[i * 128:(i + 1) * 128, b * 128:(b + 1) * 128] *= 2.0 ** int(torch.randint(-12, 13, (1,), generator=g))
+    y, s = ref.linear(ref.act_values(x), ref.weight_values(w))
+    p = q.fp8_quantize_weights(w)
+    for lo, hi in ((0, 150), (3, 4), (5, 21), (0, 100)):
+        check_product(q.linear_fp8_fused(x[lo:hi], p), y[lo:hi], s[lo:hi], k)
+    assert q.qvae_get_error() == 0
+
+
+def test_linear_of_extreme_scales(q):
+    x, w = rows(40, 384, 4), matrix((200, 384), 5)
+    y, s = ref.linear(ref.act_values(x), ref.weight_values(w))
+    for a, b in ((-100, 100), (100, -100), (60, 40), (-40, -60)):
+        xs, ws = (x.float() * 2.0 ** a).to(torch.bfloat16), (w.float() * 2.0 ** b).to(torch.bfloat16)
+        ya, sa = ref.linear(ref.act_values(xs), ref.weight_values(ws))
+        assert torch.equal(ya, y * 2.0 ** (a + b))          # nothing left the formats' ranges
+        check_product(q.linear_fp8_fused(xs, q.fp8_quantize_weights(ws)), ya, sa, 384)
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 300])
+def test_rows_and_channels_with_nan_stay_apart(q, m):
+    x, w = rows(m, 300, 9), matrix((300, 300), 10)
+    x[0, 17] = float("nan")
+    if m > 1:
+        x[m - 1, 290] = float("inf")
+    w[140, 3] = float("inf")                                # its block: channels 128..255
+    out = q.linear_fp8_fused(x, q.fp8_quantize_weights(w))
+    y, s = ref.linear(ref.act_values(x), ref.weight_values(w))
+    assert torch.isnan(out[0]).all() and torch.isnan(out[m - 1]).all() and torch.isnan(out[:, 128:256]).all()
+    assert torch.equal(torch.isnan(out), torch.isnan(y))
+    fine = ~torch.isnan(y)
+    err, tol = (out.double() - y).abs()[fine], ref.tolerance(y, s, 300)[fine]
+    assert (err <= tol).all()
+
+
+def test_zero_rows_and_zero_weights_give_the_bias(q):
+    x, w = rows(20, 256, 1), matrix((128, 256), 2)
+    b = matrix((1, 128), 3)[0]
+    x[4] = 0
+    out = q.linear_fp8_fused(x, q.fp8_quantize_weights(w), b)
+    assert torch.equal(out[4], b)
+    out = q.linear_fp8_fused(x, q.fp8_quantize_weights(torch.zeros_like(w)), b)
+    assert torch.equal(out, b.expand(20, 128))
+    assert (q.linear_fp8_fused(x, q.fp8_quantize_weights(torch.zeros_like(w))) == 0).all()
+
+
+@pytest.mark.parametrize("m,n,k,ldo", [(5, 100, 200, 104), (50, 100, 200, 111), (130, 256, 256, 320), (300, 257, 64, 257),
+                                       (600, 512, 128, 520)])
+def test_only_the_rows_and_columns_of_out_are_written(q, m, n, k, ldo):
+    x, w = rows(m, k, 1, 40), matrix((n, k), 2)
+    p = q.fp8_quantize_weights(w)
+    guard = 64
+    buf = torch.full(((m + 2 * guard) * ldo,), 7.5, dtype=torch.bfloat16, device="cuda")
+    off = guard * ldo // 8 * 8
+    out = buf[off:off + m * ldo].view(m, ldo)[:, :n]
+    got = q.linear_fp8_fused(x, p, out=out)
+    assert got.data_ptr() == out.data_ptr() and q.qvae_get_error() == 0
+    y, s = ref.linear(ref.act_values(x), ref.weight_values(w))
+    check_product(out, y, s, k)
+    out.fill_(7.5)
+    assert (buf == 7.5).all()
+
+
+def test_rows_that_do_not_start_on_16_bytes(q):
+    buf = rows(50, 1111, 8)
+    x = buf[:, :1003]                                       # odd row stride
+    w = matrix((96, 1003), 3)
+    p = q.fp8_quantize_weights(w)
+    assert torch.equal(q.linear_fp8_fused(x, p), q.linear_fp8_fused(x.contiguous(), p))
+    one = torch.zeros(50 * 1003 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(50, 1003)
+    one.copy_(x)
+    out = torch.zeros(50 * 96 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(50, 96)
+    assert torch.equal(q.linear_fp8_fused(one, p, out=out), q.linear_fp8_fused(x.contiguous(), p))
+    h = rows(30, 2 * 205, 4)                                # the up half of a row starts anywhere
+    p = q.fp8_quantize_weights(matrix((64, 205), 5))
+    wide = torch.zeros((30, 416), dtype=torch.bfloat16, device="cuda")
+    wide[:, :410] = h
+    assert torch.equal(q.linear_fp8_fused(h, p, silu_mul=True), q.linear_fp8_fused(wide[:, :410], p, silu_mul=True))
+
+
+# ---------------------------------------------------------------- grouped
+
+def spans(counts, before=0):
+    o = [before]
+    for c in counts:
+        o.append(o[-1] + c)
+    return o
+
+
+GROUPS = [
+    ([5], 0, 0), ([0, 3, 0], 0, 0), ([1, 1, 1, 1], 0, 0), ([16, 0, 17, 1, 0, 33], 2, 3), ([0, 0, 0], 0, 5),
+    ([300, 5, 0, 127, 128, 129], 0, 0), ([1] * 70, 0, 0), ([0] * 40 + [9] + [0] * 90, 1, 1), ([241, 0, 480, 239], 7, 9),
+    ([700, 1], 0, 0),
+]
+
+
+@pytest.mark.parametrize("counts,before,behind", GROUPS, ids=lambda v: str(v)[:24])
+@pytest.mark.parametrize("n,k", [(128, 128), (200, 333), (384, 1024)])
+def test_grouped_matches_each_experts_product(q, counts, before, behind, n, k):
+    e, o = len(counts), spans(counts, before)
+    m = o[-1] + behind
+    x, w, b = rows(m, k, m + n), matrix((e, n, k), n), matrix((e, n), 3)
+    p = q.fp8_quantize_weights(w)
+    offsets = torch.tensor(o, dtype=torch.int32, device="cuda")
+    for bias in (None, b):
+        out = torch.full((m, n), 3.25, dtype=torch.bfloat16, device="cuda")
+        two = out.clone()
+        q.linear_fp8_grouped_fused(x, offsets, p, bias, out=out)
+        q.linear_fp8_grouped(*q.fp8_quant_act(x), offsets, p, bias, out=two)
+        assert q.qvae_get_error() == 0
+        for t in (out, two):
+            assert (t[:before] == 3.25).all() and (t[o[-1]:] == 3.25).all()
+            for i in range(e):
+                lo, hi = o[i], o[i + 1]
+                if hi > lo:
+                    y, s = ref.linear(ref.act_values(x[lo:hi]), ref.weight_values(w[i]), None if bias is None else bias[i])
+                    check_product(t[lo:hi], y, s, k)
+
+
+def test_grouped_rows_equal_the_single_layer(q):
+    # one expert's rows give what its matrix alone gives, whatever stands beside them
+    counts = [40, 0, 100, 3]
+    x, w = rows(143, 512, 1), matrix((4, 256, 512), 2)
+    o = torch.tensor(spans(counts), dtype=torch.int32, device="cuda")
+    out = q.linear_fp8_grouped_fused(x, o, q.fp8_quantize_weights(w))
+    for i, c in enumerate(counts):
+        lo = sum(counts[:i])
+        if c:
+            y, s = ref.linear(ref.act_values(x[lo:lo + c]), ref.weight_values(w[i]))
+            check_product(out[lo:lo + c], y, s, 512)
+            one = q.linear_fp8_fused(x[lo:lo + c], q.fp8_quantize_weights(w[i]))
+            check_product(one, y, s, 512)
+
+
+@pytest.mark.parametrize("offsets", [[-5, 10, 20, 1000], [30, 20, 10, 0], [0, 1 << 30, -(1 << 30), 40], [50, 50, 50, 50]])
+def test_offsets_out_of_range_stay_inside_the_rows(q, offsets):
+    m, n, k = 40, 130, 200
+    x, w = rows(m, k, 1), matrix((3, n, k), 2)
+    buf = torch.full((m + 64, n), 3.25, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    q.linear_fp8_grouped_fused(x, off, q.fp8_quantize_weights(w), out=buf[32:32 + m])
+    assert q.qvae_get_error() == 0
+    assert (buf[:32] == 3.25).all() and (buf[32 + m:] == 3.25).all()
+    if offsets == [-5, 10, 20, 1000]:                       # clipped to 0, 10, 20, 40
+        for i, (lo, hi) in enumerate(((0, 10), (10, 20), (20, 40))):
+            y, s = ref.linear(ref.act_values(x[lo:hi]), ref.weight_values(w[i]))
+            check_product(buf[32 + lo:32 + hi], y, s, k)
+    if offsets[0] == 50:
+        assert (buf == 3.25).all()
+
+
+def test_many_experts(q):
+    e = 1024
+    g = torch.Generator().manual_seed(0)
+    counts = torch.randint(0, 3, (e,), generator=g).tolist()
+    o = spans(counts)
+    x, w = rows(o[-1], 96, 1), matrix((e, 64, 96), 2)
+    out = q.linear_fp8_grouped_fused(x, torch.tensor(o, dtype=torch.int32, device="cuda"), q.fp8_quantize_weights(w))
+    assert q.qvae_get_error() == 0
+    who = torch.repeat_interleave(torch.arange(e), torch.tensor(counts)).cuda()
+    wv = torch.stack([ref.weight_values(t) for t in w])[who]
+    xv = ref.act_values(x)
+    y = torch.einsum("mk,mnk->mn", xv, wv)
+    s = torch.einsum("mk,mnk->mn", xv.abs(), wv.abs())
+    check_product(out, y, s, 96)
+
+
+# ------------------------------------------- a feed-forward of experts, use
+
+def feed_forward(q, x, offsets, p1, p2, **kw):
+    h = q.linear_fp8_grouped_fused(x, offsets, p1, **kw)
+    return h, q.linear_fp8_grouped_fused(h, offsets, p2, silu_mul=True, **kw)
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 2, 1], [16, 1, 0, 15], [100, 0, 301, 20]])
+def test_feed_forward_of_experts(q, counts):
+    e, d, inner = len(counts), 320, 200
+    o = spans(counts)
+    x, w1, w2 = rows(o[-1], d, 1), matrix((e, 2 * inner, d), 2), matrix((e, d, inner), 3)
+    offsets = torch.tensor(o, dtype=torch.int32, device="cuda")
+    h, out = feed_forward(q, x, offsets, q.fp8_quantize_weights(w1), q.fp8_quantize_weights(w2))
+    assert q.qvae_get_error() == 0
+    for i in range(e):
+        lo, hi = o[i], o[i + 1]
+        if hi == lo:
+            continue
+        y, s = ref.linear(ref.act_values(x[lo:hi]), ref.weight_values(w1[i]))
+        check_product(h[lo:hi], y, s, d)
+        # the second product from the hidden rows as stored, so that one rounding is not counted twice; a code next to a
+        # border may take either neighbour (2^-3 of its value): where none does the product's own tolerance holds
+        v = ref.act_values(ref.silu_mul(h[lo:hi]))
+        y, s = ref.linear(v, ref.weight_values(w2[i]))
+        tol = ref.tolerance(y, s, inner) + 2.0 ** -3 * v.abs().amax(1, keepdim=True) * ref.weight_values(w2[i]).abs().amax(1)
+        assert ((out[lo:hi].double() - y).abs() <= tol).all()
+
+
+def test_graph_replay_streams_and_shared_weights(q):
+    counts = [30, 0, 4, 66]
+    offsets = torch.tensor(spans(counts), dtype=torch.int32, device="cuda")
+    xs = [rows(100, 256, s) for s in range(3)]
+    p1 = q.fp8_quantize_weights(matrix((4, 384, 256), 2))
+    p2 = q.fp8_quantize_weights(matrix((4, 256, 192), 3))
+    want = [feed_forward(q, x, offsets, p1, p2)[1] for x in xs]
+    torch.cuda.synchronize()
+    x = xs[0].clone()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = feed_forward(q, x, offsets, p1, p2)[1]
+    for i in (1, 2, 0, 0):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i])
+    # other offsets in the captured buffer
+    offsets.copy_(torch.tensor([0, 10, 60, 60, 100], dtype=torch.int32))
+    direct = feed_forward(q, x, offsets, p1, p2)[1]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, direct)
+    offsets.copy_(torch.tensor(spans(counts), dtype=torch.int32))
+    torch.cuda.synchronize()
+    # the same weights on several streams at once, each call with buffers of its own
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[feed_forward(q, xs[i], offsets, p1, p2, stream=streams[i])[1] for i in range(3)] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert q.qvae_get_error() == 0
+    for r in got:
+        for i in range(3):
+            assert torch.equal(r[i], want[i])
+
+
+def test_weights_and_inputs_written_just_before_the_call(q):
+    # what a call reads may come from the launch right before it
+    w = [matrix((256, 512), s) for s in range(2)]
+    p = [q.fp8_quantize_weights(t) for t in w]
+    x = rows(24, 512, 4)
+    want = [q.linear_fp8_fused(x, t) for t in p]
+    codes, words = q.fp8_quant_act(x)
+    live = q.Fp8Weights(p[0].wq.clone(), p[0].w_scale.clone(), 1, 256, 512)
+    for i in range(20):
+        live.w_scale.copy_(p[i % 2].w_scale)
+        live.wq.copy_(p[i % 2].wq)
+        assert torch.equal(q.linear_fp8_fused(x, live), want[i % 2])
+        live.w_scale.copy_(p[1 - i % 2].w_scale)
+        live.wq.copy_(p[1 - i % 2].wq)
+        check = q.linear_fp8(codes, words, live)
+        assert (check.double() - want[1 - i % 2].double()).abs().max() <= 0.02 * want[1 - i % 2].abs().max()
+    assert q.qvae_get_error() == 0
+
+
+def test_empty_calls(q):
+    p = q.fp8_quantize_weights(matrix((2, 64, 96), 1))
+    x = torch.empty((0, 96), dtype=torch.bfloat16, device="cuda")
+    o = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert q.linear_fp8_grouped_fused(x, o, p).shape == (0, 64)
+    assert q.linear_fp8_grouped(*q.fp8_quant_act(x), o, p).shape == (0, 64)
+    x = rows(10, 96, 1)
+    out = torch.full((10, 64), 2.0, dtype=torch.bfloat16, device="cuda")
+    q.linear_fp8_grouped_fused(x, o, p, out=out)
+    assert (out == 2.0).all()
+
+
+def test_binding_refusals(q):
+    p = q.fp8_quantize_weights(matrix((2, 64, 96), 1))
+    one = q.fp8_quantize_weights(matrix((64, 96), 1))
+    x = rows(4, 96, 1)
+    o = torch.tensor([0, 1, 4], dtype=torch.int32, device="cuda")
+    for call in (lambda: q.linear_fp8_fused(x, p),                                            # experts without offsets
+                 lambda: q.linear_fp8_fused(x[:, :95], one), lambda: q.linear_fp8_fused(x.float(), one),
+                 lambda: q.linear_fp8_fused(x, one, silu_mul=True),
+                 lambda: q.linear_fp8_fused(x, one, bias=torch.zeros(63, dtype=torch.bfloat16, device="cuda")),
+                 lambda: q.linear_fp8_fused(x, one, bias=torch.zeros(64, device="cuda")),
+                 lambda: q.linear_fp8_fused(x, one, out=torch.zeros((3, 64), dtype=torch.bfloat16, device="cuda")),
+                 lambda: q.linear_fp8_fused(x, one, out=torch.zeros((4, 64), device="cuda")),
+                 lambda: q.linear_fp8_fused(x, one, out=torch.zeros((64, 4), dtype=torch.bfloat16, device="cuda").t()),
+                 lambda: q.linear_fp8_grouped_fused(x, o.long(), p), lambda: q.linear_fp8_grouped_fused(x, o[:2], p),
+                 lambda: q.linear_fp8_grouped_fused(x, o.cpu(), p), lambda: q.linear_fp8_grouped_fused(x, None, p),
+                 lambda: q.linear_fp8_grouped_fused(x, o, p, bias=torch.zeros(64, dtype=torch.bfloat16, device="cuda")),
+                 lambda: q.linear_fp8(q.fp8_quant_act(x)[0], q.fp8_quant_act(x)[1][:, :3], one),
+                 lambda: q.linear_fp8_fused(x, one._replace(wq=one.wq[:-1]))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(q.QvaeError) as e:
+        q.linear_fp8_fused(x, one, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == q.QVAE_ERR_ARG
+    words = torch.empty(2048, dtype=torch.uint8, device="cuda")
+    with pytest.raises(q.QvaeError) as e:
+        q.linear_fp8_fused(x, one, workspace=words[8:])
+    assert e.value.status == q.QVAE_ERR_ALIGN

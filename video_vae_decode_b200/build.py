@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libqvae.so")
 LIB_DEBUG = os.path.join(HERE, "libqvae_debug.so")
 ROOT = os.path.dirname(HERE)
 SOURCES = ["qvae.cu"]
-DEPS = ["qvae.cu", "conv.cuh", "quant.cuh", "ptx.cuh"]
+DEPS = ["qvae.cu", "conv.cuh", "fp8.cuh", "quant.cuh", "ptx.cuh"]
 
 
 def nvcc_path() -> str:

@@ -17,6 +17,7 @@
 
 #include "../../include/qvae.h"
 #include "conv.cuh"
+#include "fp8.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 
@@ -51,6 +52,7 @@ int cuda_fail(cudaError_t e, const char* what) {
   } while (0)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
 int current_device(int* dev) {
   QVAE_CUDA(cudaGetDevice(dev));
@@ -283,10 +285,10 @@ int encode_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* ptr, con
 // the grid may start while its predecessor finishes and synchronises with
 // griddepcontrol.wait before touching the predecessor's results.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(KArgs...), int grid, int block, size_t smem,
+cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem,
                              cudaStream_t stream, int cluster, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -568,6 +570,140 @@ int launch_quant_from_amax(const void* x, int64_t numel, const uint32_t* amax, i
       reinterpret_cast<uint4*>(xq), xq, x_scale, zero_word);
   QVAE_CUDA(cudaGetLastError());
   return QVAE_OK;
+}
+
+// ------------------------------------- 8-bit floating-point linear layers
+
+constexpr int64_t kLinMaxRows = int64_t{1} << 30;      // rows of x in a call
+constexpr int64_t kLinMaxChannels = int64_t{1} << 20;  // N, K
+
+bool g_lin_attr_set[kMaxDevices] = {};
+
+int check_linear(int64_t E, int64_t M, int64_t N, int64_t K) {
+  if (E < 0 || M < 0 || N < 0 || K < 0) return QVAE_ERR_ARG;
+  if (E < 1 || E > qvae::kLinMaxExperts || N < 1 || N > kLinMaxChannels || K < 1 || K > kLinMaxChannels ||
+      M > kLinMaxRows)
+    return QVAE_ERR_SHAPE;
+  // 128-byte weight rows are tensor-map coordinates
+  if (E * ceil_div(N, qvae::kFp8Block) * ceil_div(K, qvae::kFp8Block) > INT32_MAX / qvae::kFp8Block)
+    return QVAE_ERR_SHAPE;
+  return QVAE_OK;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+int launch_fp8_quant(int64_t M, int64_t K, int op, const void* x, int64_t ldx, uint8_t* xq, uint32_t* x_scale,
+                     cudaStream_t stream) {
+  const int rc = check_linear(1, M, 1, K);
+  if (rc) return rc;
+  if (op != QVAE_FP8_PLAIN && op != QVAE_FP8_SILU_MUL) return QVAE_ERR_ARG;
+  if (M == 0) return QVAE_OK;
+  const bool silu = op == QVAE_FP8_SILU_MUL;
+  if (!x || !xq || !x_scale || ldx < (silu ? 2 * K : K)) return QVAE_ERR_ARG;
+  if (ldx > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
+  if (!aligned2(x) || !aligned16(xq) || !aligned16(x_scale)) return QVAE_ERR_ALIGN;
+  const int Kb = static_cast<int>(ceil_div(K, qvae::kFp8Block));
+  // 16-byte loads where every row (and the second half of one) starts on 16 bytes
+  const bool vec = aligned16(x) && (ldx % 8 == 0 || M == 1) && (!silu || K % 8 == 0);
+  using Kernel = void (*)(const uint16_t*, int64_t, int, int, int, uint8_t*, uint32_t*);
+  const Kernel kernels[4] = {qvae::fp8_quant_act_kernel<false, false>, qvae::fp8_quant_act_kernel<false, true>,
+                             qvae::fp8_quant_act_kernel<true, false>, qvae::fp8_quant_act_kernel<true, true>};
+  const dim3 grid(static_cast<unsigned>(ceil_div(M, qvae::kFp8RowsPerBlock)), static_cast<unsigned>(ceil_div(Kb, 4)));
+  QVAE_CUDA(launch_dependent(kernels[(silu ? 2 : 0) + (vec ? 1 : 0)], grid, qvae::kFp8QuantThreads, 0, stream, 1,
+                             static_cast<const uint16_t*>(x), ldx, static_cast<int>(M), static_cast<int>(K), Kb, xq,
+                             x_scale));
+  return QVAE_OK;
+}
+
+// offsets null: one span of M rows.
+int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq, const uint32_t* x_scale,
+                  const int32_t* offsets, const uint8_t* wq, const uint8_t* w_scale, const void* bias, void* out,
+                  int64_t ldo, cudaStream_t stream) {
+  int rc = check_linear(E, M, N, K);
+  if (rc) return rc;
+  if (M == 0) return QVAE_OK;
+  if (!xq || !x_scale || !wq || !w_scale || !out || ldo < N) return QVAE_ERR_ARG;
+  if (ldo > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
+  if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(wq) || !aligned16(w_scale) || !aligned2(bias) ||
+      !aligned2(out))
+    return QVAE_ERR_ALIGN;
+  int dev, sms;
+  if ((rc = current_device(&dev))) return rc;
+  if ((rc = sm_count(dev, &sms))) return rc;
+
+  qvae::LinArgs a = {};
+  a.E = static_cast<int>(E);
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.Kb = static_cast<int>(ceil_div(K, qvae::kFp8Block));
+  a.last_ksteps = static_cast<int>(ceil_div(K - int64_t{a.Kb - 1} * qvae::kFp8Block, 32));
+  a.nblk = static_cast<int>(ceil_div(N, qvae::kFp8Block));
+  a.kgroups = (a.Kb + 3) / 4;
+  const int64_t rows = ceil_div(M, E);  // of an expert, on average
+  a.NT = static_cast<int>(std::min<int64_t>(qvae::kLinMaxNT, ceil_div(rows, 16) * 16));
+  if ((ceil_div(M, a.NT) + E) * a.nblk > INT32_MAX / 2) return QVAE_ERR_SHAPE;
+  const int box_rows = (a.NT + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
+  a.stage_bytes = qvae::kLinATile + static_cast<uint32_t>(box_rows) * 128u;
+  const uint32_t rest = 1024u + qvae::kLinBars + 8u + 4u * static_cast<uint32_t>(3 * E + 1);
+  a.stages = std::min<int>(qvae::kLinMaxStages, (kSmemLimit - rest) / a.stage_bytes);
+  const uint32_t smem = rest + a.stages * a.stage_bytes;
+  // two accumulators (the epilogue reads 32 columns at a time) and two sets of scale words
+  a.acc_cols = static_cast<uint32_t>(a.NT);
+  a.sf_col = a.acc_cols + static_cast<uint32_t>(box_rows);
+  a.tmem_cols = 32;
+  while (a.tmem_cols < a.sf_col + 16) a.tmem_cols <<= 1;
+  a.offsets = offsets;
+  a.x_scale = x_scale;
+  a.w_scale = reinterpret_cast<const uint32_t*>(w_scale);
+  a.bias = static_cast<const __nv_bfloat16*>(bias);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.ldo = ldo;
+  a.wait_limit_ns = g_wait_limit_ns;
+
+  CUtensorMap tmap_x, tmap_w;
+  {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.Kb) * 128u, static_cast<cuuint64_t>(M)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.Kb) * 128u};
+    const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(qvae::kLinBoxRows)};
+    if ((rc = encode_map(&tmap_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, dims, strides, box, 2, CU_TENSOR_MAP_SWIZZLE_128B)))
+      return rc;
+  }
+  {
+    const cuuint64_t dims[2] = {128u, static_cast<cuuint64_t>(E) * a.nblk * a.Kb * qvae::kFp8Block};
+    const cuuint64_t strides[1] = {128u};
+    const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(qvae::kFp8Block)};
+    if ((rc = encode_map(&tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, dims, strides, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE)))
+      return rc;
+  }
+  if (!g_lin_attr_set[dev]) {
+    QVAE_CUDA(cudaFuncSetAttribute(qvae::linear_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
+    g_lin_attr_set[dev] = true;
+  }
+  const int64_t most_tiles = (offsets ? ceil_div(M, a.NT) + std::min(E, M) : ceil_div(M, a.NT)) * a.nblk;
+  const int grid = static_cast<int>(std::min<int64_t>(most_tiles, sms));
+  QVAE_CUDA(launch_dependent(qvae::linear_fp8_kernel, dim3(grid), qvae::kLinThreads, smem, stream, 1, tmap_x, tmap_w, a));
+  return QVAE_OK;
+}
+
+// The layer from bf16 rows: the quantiser into the workspace, then the product.
+int launch_linear_fused(int64_t E, int64_t M, int64_t N, int64_t K, int op, const void* x, int64_t ldx,
+                        const int32_t* offsets, const uint8_t* wq, const uint8_t* w_scale, const void* bias, void* out,
+                        int64_t ldo, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  int rc = check_linear(E, M, N, K);
+  if (rc) return rc;
+  if (op != QVAE_FP8_PLAIN && op != QVAE_FP8_SILU_MUL) return QVAE_ERR_ARG;
+  if (M == 0) return QVAE_OK;
+  // everything the second launch refuses is refused before the first
+  if (!wq || !w_scale || !out || ldo < N || !workspace || workspace_bytes < qvae_fp8_workspace_bytes(M, K))
+    return QVAE_ERR_ARG;
+  if (ldo > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
+  if (!aligned16(wq) || !aligned16(w_scale) || !aligned2(bias) || !aligned2(out) || !aligned16(workspace))
+    return QVAE_ERR_ALIGN;
+  uint8_t* const xq = static_cast<uint8_t*>(workspace);
+  uint32_t* const x_scale = reinterpret_cast<uint32_t*>(xq + round256(qvae_fp8_code_bytes(M, K)));
+  if ((rc = launch_fp8_quant(M, K, op, x, ldx, xq, x_scale, stream))) return rc;
+  return launch_linear(E, M, N, K, xq, x_scale, offsets, wq, w_scale, bias, out, ldo, stream);
 }
 
 }  // namespace
@@ -927,6 +1063,81 @@ int qvae_decode_layers(const qvae_layer* layers, int32_t n, void* workspace,
     if (rc) return rc;
   }
   return QVAE_OK;
+}
+
+size_t qvae_fp8_packed_weight_bytes(int32_t E, int32_t N, int32_t K) {
+  if (check_linear(E, 0, N, K)) return 0;
+  return static_cast<size_t>(E) * ceil_div(N, qvae::kFp8Block) * ceil_div(K, qvae::kFp8Block) * qvae::kLinATile;
+}
+
+size_t qvae_fp8_weight_scale_bytes(int32_t E, int32_t N, int32_t K) {
+  if (check_linear(E, 0, N, K)) return 0;
+  return static_cast<size_t>(E) * ceil_div(N, qvae::kFp8Block) * ceil_div(K, 4 * qvae::kFp8Block) * 4;
+}
+
+int qvae_fp8_quantize_weights(int32_t E, int32_t N, int32_t K, const void* w_bf16, uint8_t* wq_packed,
+                              uint8_t* w_scale, void* stream) {
+  const int rc = check_linear(E, 0, N, K);
+  if (rc) return rc;
+  if (!w_bf16 || !wq_packed || !w_scale) return QVAE_ERR_ARG;
+  if (!aligned2(w_bf16) || !aligned16(wq_packed) || !aligned16(w_scale)) return QVAE_ERR_ALIGN;
+  const int nblk = static_cast<int>(ceil_div(N, qvae::kFp8Block)), Kb = static_cast<int>(ceil_div(K, qvae::kFp8Block));
+  const auto kernel = K % 8 == 0 && aligned16(w_bf16) ? qvae::fp8_pack_weights_kernel<true> : qvae::fp8_pack_weights_kernel<false>;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  kernel<<<static_cast<unsigned>(static_cast<int64_t>(E) * nblk * Kb), qvae::kFp8PackThreads, 0, st>>>(
+      static_cast<const uint16_t*>(w_bf16), N, K, nblk, Kb, wq_packed, w_scale);
+  QVAE_CUDA(cudaGetLastError());
+  return QVAE_OK;
+}
+
+size_t qvae_fp8_code_bytes(int64_t M, int32_t K) {
+  if (check_linear(1, M, 1, K)) return 0;
+  return static_cast<size_t>(M) * ceil_div(K, qvae::kFp8Block) * qvae::kFp8Block;
+}
+
+size_t qvae_fp8_scale_bytes(int64_t M, int32_t K) {
+  if (check_linear(1, M, 1, K)) return 0;
+  return static_cast<size_t>(M) * ceil_div(K, 4 * qvae::kFp8Block) * 4;
+}
+
+size_t qvae_fp8_workspace_bytes(int64_t M, int32_t K) {
+  return round256(qvae_fp8_code_bytes(M, K)) + round256(qvae_fp8_scale_bytes(M, K));
+}
+
+int qvae_fp8_quant_act(int64_t M, int32_t K, int32_t op, const void* x_bf16, int64_t ldx, uint8_t* xq, uint32_t* x_scale,
+                       void* stream) {
+  return launch_fp8_quant(M, K, op, x_bf16, ldx, xq, x_scale, static_cast<cudaStream_t>(stream));
+}
+
+int qvae_linear_fp8(int64_t M, int32_t N, int32_t K, const uint8_t* xq, const uint32_t* x_scale,
+                    const uint8_t* wq_packed, const uint8_t* w_scale, const void* bias_bf16, void* out_bf16, int64_t ldo,
+                    void* stream) {
+  return launch_linear(1, M, N, K, xq, x_scale, nullptr, wq_packed, w_scale, bias_bf16, out_bf16, ldo,
+                       static_cast<cudaStream_t>(stream));
+}
+
+int qvae_linear_fp8_grouped(int32_t E, int64_t M, int32_t N, int32_t K, const uint8_t* xq, const uint32_t* x_scale,
+                            const int32_t* offsets, const uint8_t* wq_packed, const uint8_t* w_scale,
+                            const void* bias_bf16, void* out_bf16, int64_t ldo, void* stream) {
+  if (M > 0 && !offsets) return QVAE_ERR_ARG;
+  return launch_linear(E, M, N, K, xq, x_scale, offsets, wq_packed, w_scale, bias_bf16, out_bf16, ldo,
+                       static_cast<cudaStream_t>(stream));
+}
+
+int qvae_linear_fp8_fused(int64_t M, int32_t N, int32_t K, int32_t op, const void* x_bf16, int64_t ldx,
+                          const uint8_t* wq_packed, const uint8_t* w_scale, const void* bias_bf16, void* out_bf16,
+                          int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
+  return launch_linear_fused(1, M, N, K, op, x_bf16, ldx, nullptr, wq_packed, w_scale, bias_bf16, out_bf16, ldo,
+                             workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int qvae_linear_fp8_grouped_fused(int32_t E, int64_t M, int32_t N, int32_t K, int32_t op, const void* x_bf16,
+                                  int64_t ldx, const int32_t* offsets, const uint8_t* wq_packed, const uint8_t* w_scale,
+                                  const void* bias_bf16, void* out_bf16, int64_t ldo, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (M > 0 && !offsets) return QVAE_ERR_ARG;
+  return launch_linear_fused(E, M, N, K, op, x_bf16, ldx, offsets, wq_packed, w_scale, bias_bf16, out_bf16, ldo,
+                             workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int qvae_get_error(void* stream) {

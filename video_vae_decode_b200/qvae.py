@@ -8,9 +8,10 @@ Each wrapper raises ``QvaeError`` on a non-zero status.  ``lib()`` raises if
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -36,7 +37,13 @@ EXPORTS = (
     "qvae_packed_weight_bytes_bf16", "qvae_pack_weights_bf16", "qvae_causal_conv3d_bf16",
     "qvae_causal_conv3d_bf16_acc32", "qvae_causal_conv3d_w8a8_fused", "qvae_causal_conv3d_w8a8_fused_acc32",
     "qvae_set_fused_quant",
+    "qvae_fp8_packed_weight_bytes", "qvae_fp8_weight_scale_bytes", "qvae_fp8_quantize_weights",
+    "qvae_fp8_code_bytes", "qvae_fp8_scale_bytes", "qvae_fp8_workspace_bytes", "qvae_fp8_quant_act",
+    "qvae_linear_fp8", "qvae_linear_fp8_grouped", "qvae_linear_fp8_fused", "qvae_linear_fp8_grouped_fused",
 )
+
+# qvae_fp8_op: what a linear layer quantises of its rows
+QVAE_FP8_PLAIN, QVAE_FP8_SILU_MUL = 0, 1
 
 
 class QvaeError(RuntimeError):
@@ -102,6 +109,18 @@ def lib():
             "qvae_set_conv_cta_limit": ([i32], ctypes.c_int),
             "qvae_set_fused_quant": ([i32], ctypes.c_int),
             "qvae_get_conv_tiling": ([ctypes.POINTER(qvae_shape), i32, ctypes.POINTER(i32)], ctypes.c_int),
+            "qvae_fp8_packed_weight_bytes": ([i32, i32, i32], sz),
+            "qvae_fp8_weight_scale_bytes": ([i32, i32, i32], sz),
+            "qvae_fp8_quantize_weights": ([i32, i32, i32, p, p, p, p], ctypes.c_int),
+            "qvae_fp8_code_bytes": ([i64, i32], sz),
+            "qvae_fp8_scale_bytes": ([i64, i32], sz),
+            "qvae_fp8_workspace_bytes": ([i64, i32], sz),
+            "qvae_fp8_quant_act": ([i64, i32, i32, p, i64, p, p, p], ctypes.c_int),
+            "qvae_linear_fp8": ([i64, i32, i32, p, p, p, p, p, p, i64, p], ctypes.c_int),
+            "qvae_linear_fp8_grouped": ([i32, i64, i32, i32, p, p, p, p, p, p, p, i64, p], ctypes.c_int),
+            "qvae_linear_fp8_fused": ([i64, i32, i32, i32, p, i64, p, p, p, p, i64, p, sz, p], ctypes.c_int),
+            "qvae_linear_fp8_grouped_fused": ([i32, i64, i32, i32, i32, p, i64, p, p, p, p, p, i64, p, sz, p],
+                                              ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -415,6 +434,217 @@ def qvae_decode_layers(layers, workspace: torch.Tensor, stream=None) -> None:
     _check("qvae_decode_layers",
            lib().qvae_decode_layers(layers, len(layers), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# --------------------------------- 8-bit floating-point linear layers
+#
+# Tensors on another device than the current one run on their own device (its
+# current stream by default).  What a wrapper allocates is allocated on the
+# stream that the call runs on.
+
+class Fp8Weights(NamedTuple):
+    """Packed e4m3 weights of E matrices [N, K] (qvae_fp8_quantize_weights)."""
+    wq: torch.Tensor       # uint8, qvae_fp8_packed_weight_bytes(E, N, K)
+    w_scale: torch.Tensor  # uint8, qvae_fp8_weight_scale_bytes(E, N, K)
+    E: int
+    N: int
+    K: int
+
+
+def qvae_fp8_packed_weight_bytes(E: int, N: int, K: int) -> int:
+    return int(lib().qvae_fp8_packed_weight_bytes(E, N, K))
+
+
+def qvae_fp8_weight_scale_bytes(E: int, N: int, K: int) -> int:
+    return int(lib().qvae_fp8_weight_scale_bytes(E, N, K))
+
+
+def qvae_fp8_code_bytes(M: int, K: int) -> int:
+    return int(lib().qvae_fp8_code_bytes(M, K))
+
+
+def qvae_fp8_scale_bytes(M: int, K: int) -> int:
+    return int(lib().qvae_fp8_scale_bytes(M, K))
+
+
+def qvae_fp8_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().qvae_fp8_workspace_bytes(M, K))
+
+
+def _want(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _buffer(t: torch.Tensor, dtype: torch.dtype, count: int, device: torch.device, name: str) -> int:
+    """Address of a contiguous tensor of at least `count` elements."""
+    _want(t.dtype == dtype and t.device == device and t.is_contiguous() and t.numel() >= count,
+          f"{name}: a contiguous {dtype} tensor of {count} elements on {device} is needed")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor, columns: int, device: torch.device, name: str) -> int:
+    """Elements between the rows of a bf16 matrix [M, columns] whose columns are adjacent."""
+    _want(t.dtype == torch.bfloat16 and t.device == device and t.dim() == 2 and t.shape[1] == columns,
+          f"{name}: a bf16 matrix of {columns} columns on {device} is needed")
+    ld = t.stride(0) if t.shape[0] > 1 else columns
+    _want((columns == 1 or t.stride(1) == 1) and ld >= columns,
+          f"{name}: rows of adjacent columns that do not overlap are needed")
+    return ld
+
+
+def _on_stream(device: torch.device, stream):
+    """Context for a call on `device` and `stream` (None: the device's current stream), and that stream's handle."""
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+        if device.index == torch.cuda.current_device():
+            return contextlib.nullcontext(), handle
+        return torch.cuda.device(device), handle
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
+    _want(stream.device == device, f"the stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _cuda(t: torch.Tensor, name: str) -> torch.device:
+    _want(isinstance(t, torch.Tensor) and t.is_cuda, f"{name}: a CUDA tensor is needed")
+    return t.device
+
+
+def fp8_quantize_weights(w: torch.Tensor, stream=None) -> Fp8Weights:
+    """Quantise and pack bf16 weights [N, K] or, one matrix to an expert, [E, N, K]."""
+    device = _cuda(w, "w")
+    _want(w.dtype == torch.bfloat16 and w.dim() in (2, 3) and w.is_contiguous(),
+          "w: contiguous bf16 weights [N, K] or [E, N, K] are needed")
+    E, N, K = (1, *w.shape) if w.dim() == 2 else w.shape
+    ctx, handle = _on_stream(device, stream)
+    with ctx:
+        wq = torch.empty(qvae_fp8_packed_weight_bytes(E, N, K), dtype=torch.uint8, device=device)
+        ws = torch.empty(qvae_fp8_weight_scale_bytes(E, N, K), dtype=torch.uint8, device=device)
+        _check("qvae_fp8_quantize_weights",
+               lib().qvae_fp8_quantize_weights(E, N, K, w.data_ptr(), wq.data_ptr(), ws.data_ptr(), handle))
+    return Fp8Weights(wq, ws, E, N, K)
+
+
+def fp8_workspace(M: int, K: int, device="cuda") -> torch.Tensor:
+    """Scratch of the _fused layers for M rows of K input channels."""
+    return torch.empty(max(16, qvae_fp8_workspace_bytes(M, K)), dtype=torch.uint8, device=device)
+
+
+def fp8_quant_act(x: torch.Tensor, silu_mul: bool = False, stream=None):
+    """Codes (uint8 [M, 128 ceil(K/128)]) and scale words (int32 [ceil(K/512), M]) of bf16 rows x [M, K]
+    (silu_mul: [M, 2 K], of which silu(x[:, :K]) * x[:, K:] is quantised)."""
+    device = _cuda(x, "x")
+    _want(x.dim() == 2 and x.shape[1] >= 1 and not (silu_mul and x.shape[1] % 2),
+          "x: a matrix is needed, with an even number of columns for silu_mul")
+    M, columns = x.shape
+    K = columns // 2 if silu_mul else columns
+    ld = _row_stride(x, columns, device, "x")
+    ctx, handle = _on_stream(device, stream)
+    with ctx:
+        xq = torch.empty((M, -(-K // 128) * 128), dtype=torch.uint8, device=device)
+        xs = torch.empty((-(-K // 512), M), dtype=torch.int32, device=device)
+        _check("qvae_fp8_quant_act",
+               lib().qvae_fp8_quant_act(M, K, QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN, x.data_ptr(), ld,
+                                        xq.data_ptr(), xs.data_ptr(), handle))
+    return xq, xs
+
+
+def _layer(device, weights, M, bias, out, offsets):
+    """Checks what every product takes; (row stride of out, addresses of weights, scales, bias, offsets)."""
+    E, N, K = weights.E, weights.N, weights.K
+    if offsets is None:
+        _want(E == 1, f"the weights hold {E} experts: use the grouped product")
+        po = None
+    else:
+        po = _buffer(offsets, torch.int32, E + 1, device, "offsets")
+    pb = None
+    if bias is not None:
+        _want(tuple(bias.shape) in ((E, N), (N,) if E == 1 else (E, N)), f"bias: [N] or [E, N] is needed, N = {N}, E = {E}")
+        pb = _buffer(bias, torch.bfloat16, E * N, device, "bias")
+    ldo = N
+    if out is not None:
+        ldo = _row_stride(out, N, device, "out")
+        _want(out.shape[0] == M, f"out: {M} rows are needed")
+    blocks = E * -(-N // 128)
+    return (ldo, _buffer(weights.wq, torch.uint8, blocks * -(-K // 128) * 16384, device, "weights.wq"),
+            _buffer(weights.w_scale, torch.uint8, blocks * -(-K // 512) * 4, device, "weights.w_scale"), pb, po)
+
+
+def _product(name, xq, x_scale, weights, bias, out, offsets, stream):
+    device = _cuda(xq, "xq")
+    M = xq.shape[0]
+    K = weights.K
+    px = _buffer(xq, torch.uint8, M * -(-K // 128) * 128, device, "xq")
+    ps = _buffer(x_scale, torch.int32, M * -(-K // 512), device, "x_scale")
+    _want(xq.dim() == 2 and xq.shape[1] == -(-K // 128) * 128, f"xq: codes of {K} input channels are needed")
+    ldo, pw, pws, pb, po = _layer(device, weights, M, bias, out, offsets)
+    ctx, handle = _on_stream(device, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty((M, weights.N), dtype=torch.bfloat16, device=device)
+        if offsets is None:
+            status = lib().qvae_linear_fp8(M, weights.N, K, px, ps, pw, pws, pb, out.data_ptr(), ldo, handle)
+        else:
+            status = lib().qvae_linear_fp8_grouped(weights.E, M, weights.N, K, px, ps, po, pw, pws, pb,
+                                                   out.data_ptr(), ldo, handle)
+    _check(name, status)
+    return out
+
+
+def linear_fp8(xq: torch.Tensor, x_scale: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """bf16 [M, N] of quantised rows (fp8_quant_act) and one weight matrix."""
+    return _product("qvae_linear_fp8", xq, x_scale, weights, bias, out, None, stream)
+
+
+def linear_fp8_grouped(xq: torch.Tensor, x_scale: torch.Tensor, offsets: torch.Tensor, weights: Fp8Weights,
+                       bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """bf16 [M, N] of quantised rows sorted by expert: rows offsets[e]..offsets[e+1]-1 (int32, on the device) meet
+    expert e's matrix; other rows of out are left as they are."""
+    _want(offsets is not None, "offsets: an int32 tensor is needed")
+    return _product("qvae_linear_fp8_grouped", xq, x_scale, weights, bias, out, offsets, stream)
+
+
+def _fused(name, x, weights, bias, silu_mul, out, workspace, offsets, stream):
+    device = _cuda(x, "x")
+    K = weights.K
+    ldx = _row_stride(x, 2 * K if silu_mul else K, device, "x")
+    M = x.shape[0]
+    ldo, pw, pws, pb, po = _layer(device, weights, M, bias, out, offsets)
+    op = QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN
+    ctx, handle = _on_stream(device, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty((M, weights.N), dtype=torch.bfloat16, device=device)
+        if workspace is None:
+            workspace = fp8_workspace(M, K, device)
+        pk = _buffer(workspace, torch.uint8, 0, device, "workspace")
+        if offsets is None:
+            status = lib().qvae_linear_fp8_fused(M, weights.N, K, op, x.data_ptr(), ldx, pw, pws, pb, out.data_ptr(),
+                                                 ldo, pk, workspace.numel(), handle)
+        else:
+            status = lib().qvae_linear_fp8_grouped_fused(weights.E, M, weights.N, K, op, x.data_ptr(), ldx, po, pw, pws,
+                                                         pb, out.data_ptr(), ldo, pk, workspace.numel(), handle)
+    _check(name, status)
+    return out
+
+
+def linear_fp8_fused(x: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None, silu_mul: bool = False,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """bf16 [M, N] of bf16 rows x [M, K] (silu_mul: [M, 2 K] = [gate | up]), quantised on the way."""
+    return _fused("qvae_linear_fp8_fused", x, weights, bias, silu_mul, out, workspace, None, stream)
+
+
+def linear_fp8_grouped_fused(x: torch.Tensor, offsets: torch.Tensor, weights: Fp8Weights,
+                             bias: Optional[torch.Tensor] = None, silu_mul: bool = False,
+                             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """linear_fp8_grouped of bf16 rows, quantised on the way."""
+    _want(offsets is not None, "offsets: an int32 tensor is needed")
+    return _fused("qvae_linear_fp8_grouped_fused", x, weights, bias, silu_mul, out, workspace, offsets, stream)
 
 
 # ---------------------------------------------------------------- control
