@@ -439,9 +439,9 @@ int qvae_linear_fp8(int64_t M, int32_t N, int32_t K, const uint8_t* xq, const ui
  * offsets[e] .. offsets[e + 1] - 1 meet matrix e (and bias row e).
  *   offsets   [E + 1] int32 on the DEVICE, not decreasing, 0 <= . <= M; an expert
  *             without rows costs nothing.  Rows before offsets[0] and from
- *             offsets[E] on are left as they are.  (Values outside 0..M are
- *             clipped and a span that would end before it starts is empty: no
- *             access leaves the M rows.)
+ *             offsets[E] on are left as they are.  (A value outside 0..M
+ *             is clipped and one below an earlier one counts as that one: no
+ *             access leaves the M rows and no row is written twice.)
  *   wq_packed, w_scale   from qvae_fp8_quantize_weights with this E.
  *   bias_bf16 [E][N] or NULL.
  */
@@ -516,6 +516,21 @@ int qvae_set_conv_tiling(int32_t MS, int32_t NT, int32_t SA, int32_t SB, int32_t
  * A small cap makes each CTA walk several tiles of a small problem.
  */
 int qvae_set_conv_cta_limit(int32_t max_ctas);
+
+/*
+ * Tiling override of the linear layers for tuning and tests (process-wide, not
+ * thread-safe).  A tile is up to NT rows by 128 output channels of a CTA, or by
+ * 256 of a CTA pair.
+ *   NT        a multiple of 16, <= 240 (single CTAs take at most 128)
+ *   mode      1 = single CTAs, 2 = CTA pairs (cta_group::2)
+ *   max_ctas  cap on the CTAs of a launch
+ * Zero = automatic.
+ */
+int qvae_set_linear_tiling(int32_t NT, int32_t mode, int32_t max_ctas);
+
+/* The tiling that a product of these sizes would use: out[0] = NT, out[1] =
+ * mode.  E = 0: a single layer; else grouped by E experts. */
+int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* out2);
 
 /*
  * How qvae_decode_layers runs quantised layers (process-wide, tuning and

@@ -480,3 +480,34 @@ def test_binding_refusals(q):
     with pytest.raises(q.QvaeError) as e:
         q.linear_fp8_fused(x, one, workspace=words[8:])
     assert e.value.status == q.QVAE_ERR_ALIGN
+
+
+# ---------------------------------------------------------------- tilings
+
+@pytest.mark.parametrize("mode", [1, 2])
+@pytest.mark.parametrize("nt", [16, 48, 112, 128, 208, 240])
+@pytest.mark.parametrize("ctas", [0, 2])
+def test_every_tiling_gives_the_same_products(q, mode, nt, ctas):
+    if mode == 1 and nt > 128:
+        pytest.skip("single CTAs take at most 128 rows")
+    try:
+        q.qvae_set_linear_tiling(nt, mode, ctas)
+        for m, n, k in ((1, 128, 128), (37, 300, 700), (300, 129, 1100), (500, 520, 96)):
+            x, w, b = rows(m, k, m), matrix((n, k), n), matrix((1, n), 3)[0]
+            out = q.linear_fp8_fused(x, q.fp8_quantize_weights(w), b)
+            assert q.qvae_get_error() == 0
+            y, s = ref.linear(ref.act_values(x), ref.weight_values(w), b)
+            check_product(out, y, s, k)
+        counts = [100, 0, 1, 17, 260, 0, 33]
+        o = spans(counts, 3)
+        x, w = rows(o[-1] + 2, 600, 1), matrix((7, 300, 600), 2)
+        out = torch.full((o[-1] + 2, 300), 3.25, dtype=torch.bfloat16, device="cuda")
+        q.linear_fp8_grouped_fused(x, torch.tensor(o, dtype=torch.int32, device="cuda"), q.fp8_quantize_weights(w), out=out)
+        assert q.qvae_get_error() == 0
+        assert (out[:3] == 3.25).all() and (out[o[-1]:] == 3.25).all()
+        for i in range(7):
+            if counts[i]:
+                y, s = ref.linear(ref.act_values(x[o[i]:o[i + 1]]), ref.weight_values(w[i]))
+                check_product(out[o[i]:o[i + 1]], y, s, 600)
+    finally:
+        q.qvae_set_linear_tiling()

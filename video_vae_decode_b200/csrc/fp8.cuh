@@ -200,16 +200,29 @@ __global__ void __launch_bounds__(kFp8PackThreads)
 // ------------------------------------------------------------- tensor cores
 
 // D[tmem] (+)= sum over 32 k of 2^(sfa + sfb) A[smem] * B[smem]^T, e4m3 x e4m3 -> fp32, one
-// E8M0 scale per row of A and of B taken from TMEM (byte a_sf / b_sf of the scale word).
+// E8M0 scale per row of A and of B taken from TMEM (a byte of the scale words, by the
+// instruction descriptor).  kPair: by a CTA pair, as in mma_i8_pair; each CTA's TMEM holds the
+// scales of its own 128 rows of A and of all rows of B.
+template <bool kPair>
 __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
+  if (kPair) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  }
 }
 
 // Instruction descriptor of kind::mxf8f6f4: e4m3 x e4m3, both operands K-major, E8M0 scales,
@@ -222,10 +235,29 @@ __device__ __forceinline__ uint32_t idesc_mxf8(uint32_t M, uint32_t N, uint32_t 
          | (sf << 29);        // A's scale byte
 }
 
-// This warp's 32 lanes of four or eight TMEM columns: lane l gets the words of thread l.
+// This warp's 32 lanes of four TMEM columns: lane l gets the words of thread l.
 __device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint32_t* w) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(w[0]), "r"(w[1]),
                "r"(w[2]), "r"(w[3])
+               : "memory");
+}
+// 16 lanes x 32 columns of TMEM as 2 x 4 pieces of 8 lanes x 8 columns: register pair (2 i, 2 i + 1) of piece
+// i = 2 c + h holds lane 8 h + l / 4, columns 8 c + 2 (l % 4) and the next.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed, to the rows whose addresses the lanes give (lane 8 i + j: row j of
+// matrix i): thread l's word i goes to rows 2 (l % 4) and the next, column l / 4, of matrix i.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3])
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -236,10 +268,12 @@ struct LinArgs {
   int E, M, N, K;
   int Kb, last_ksteps;   // 128-channel blocks; 32-channel steps in the last one
   int nblk, kgroups;     // 128-channel output blocks; groups of four 128-channel blocks (one scale word)
+  int tiles_n;           // output tiles: blocks, or pairs of them
   int NT;                // most rows of a tile (a multiple of 16)
   int stages;
   uint32_t stage_bytes;  // 16 KB of weights + the rows' codes
   uint32_t acc_cols, sf_col, tmem_cols;
+  int vec_out;           // rows of out start on 16 bytes
   const int32_t* offsets;    // [E + 1] row offsets of the experts, or null (one span of M rows)
   const uint32_t* x_scale;   // [kgroups][M]
   const uint32_t* w_scale;   // [E][nblk][kgroups]
@@ -252,11 +286,18 @@ struct LinArgs {
 constexpr int kLinScaleWarps = 4, kLinEpiWarps = 4;
 constexpr int kLinThreads = 32 * (2 + kLinScaleWarps + kLinEpiWarps);
 constexpr int kLinMaxStages = 12;
-constexpr int kLinMaxNT = 128;
 constexpr int kLinMaxExperts = 1024;
 constexpr int kLinBoxRows = 32;                        // rows of one TMA box of codes
+constexpr int kLinSpanGroup = 16;                      // row spans walked under each output tile (see LinTiles)
 constexpr uint32_t kLinATile = kFp8Block * kFp8Block;  // bytes of one weight tile
 constexpr uint32_t kLinBars = 8 * (2 * kLinMaxStages + 4 + 4 + 1);
+constexpr uint32_t kLinEpiBuf = 2048;                  // an epilogue warp's 32 rows x 32 channels of bf16
+// Most rows of a tile: two accumulators and two sets of scale words (4 columns of weights', 1 per 32 rows) fit the 512
+// columns of TMEM.
+template <bool kPair>
+constexpr int kLinMaxNT = kPair ? 240 : 128;
+template <bool kPair>
+constexpr int kLinSfCols = kPair ? 12 : 8;  // columns of one set of scale words
 
 struct LinTile {
   int e, nb, row0, rows;
@@ -264,24 +305,29 @@ struct LinTile {
 };
 
 // The tiles of a launch: for each expert, its rows in spans of at most NT (as
-// even as multiples of 16 allow), and for each span every output block.
+// even as multiples of 16 allow), and for each span every output tile.
 // `first` [E + 1]: spans before expert e; `start` [E]: its first row; `count`
 // [E]: its rows.  Tiles are walked in increasing order, so the expert is found
-// by moving on from the last one.
+// by moving on from the last one.  Inside an expert the order is: groups of
+// kLinSpanGroup spans; output tiles; spans of the group -- what runs at one
+// time then shares both its weights and its rows out of L2.
 struct LinTiles {
   const int *first, *start, *count;
-  int E, nblk;
+  int E, tiles_n;
   int e = 0;
-  __device__ __forceinline__ int total() const { return first[E] * nblk; }
+  __device__ __forceinline__ int total() const { return first[E] * tiles_n; }
   __device__ __forceinline__ LinTile at(int tile) {
-    while (tile >= first[e + 1] * nblk) ++e;
+    while (tile >= first[e + 1] * tiles_n) ++e;
     const int spans = first[e + 1] - first[e];
-    const int local = tile - first[e] * nblk;
+    const int local = tile - first[e] * tiles_n;
+    const int full = kLinSpanGroup * tiles_n;
+    const int g0 = local / full * kLinSpanGroup, in = local % full;
+    const int gs = min(kLinSpanGroup, spans - g0);
     LinTile t;
     t.e = e;
-    t.nb = local / spans;
+    t.nb = in / gs;
     const int per = ((count[e] + spans - 1) / spans + 15) & ~15;
-    const int s = local % spans;
+    const int s = g0 + in % gs;
     t.row0 = start[e] + s * per;
     t.rows = min(per, count[e] - s * per);
     t.n = (t.rows + 15) & ~15;
@@ -298,6 +344,13 @@ struct LinTiles {
 // issues the MMAs, warps 2-5 write the scale words of each group of four
 // 128-channel blocks into TMEM (every lane quarter holds a copy: warp % 4 is
 // the quarter a warp can reach), warps 6-9 write the outputs.
+//
+// kPair: a CTA pair runs the tensor cores' cta_group::2 path.  A tile is then
+// 256 output channels; each CTA loads its own 128 rows of weights and half of
+// the rows' codes, and writes the outputs of its own channels.  The leader
+// issues the MMAs; loads and scale words of both are counted on its barriers,
+// and its commits arrive on the barriers of both.
+template <bool kPair>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const LinArgs a) {
@@ -305,7 +358,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  const uint32_t bars = base + static_cast<uint32_t>(a.stages) * a.stage_bytes;
+  const uint32_t epi_stage = base + static_cast<uint32_t>(a.stages) * a.stage_bytes;
+  const uint32_t bars = epi_stage + kLinEpiWarps * kLinEpiBuf;
   const uint32_t full = bars, empty = full + 8 * kLinMaxStages;
   const uint32_t sf_full = empty + 8 * kLinMaxStages, sf_empty = sf_full + 16;
   const uint32_t acc_full = sf_empty + 16, acc_empty = acc_full + 16;
@@ -319,6 +373,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = a.wait_limit_ns;
+  constexpr int kCtas = kPair ? 2 : 1;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;  // 0 = leader of the pair
+  const bool leader = rank == 0;
+  const int first_tile = kPair ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int tile_step = kPair ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
 
   if (threadIdx.x == 0) {
     prefetch_tmap(&tmap_x);
@@ -328,65 +387,93 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(sf_full + 8 * i, kLinScaleWarps);
+      mbar_init(sf_full + 8 * i, kCtas * kLinScaleWarps);
       mbar_init(sf_empty + 8 * i, 1);
       mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_empty + 8 * i, kLinEpiWarps);
+      mbar_init(acc_empty + 8 * i, kCtas * kLinEpiWarps);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), a.tmem_cols);
+  if (warp == 1) {
+    if (kPair) {
+      tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), a.tmem_cols);
+    } else {
+      tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), a.tmem_cols);
+    }
+  }
   grid_dependency_wait();
   grid_dependents_launch();  // only now: a kernel behind this one may rely on all that came before this one
   if (warp == 2) {
-    // spans of each expert; offsets outside 0..M or decreasing are taken as empty or clipped
-    int sum = 0;
+    // spans of each expert; an offset outside 0..M is clipped, one below an earlier one counts as that one
+    int sum = 0, top = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      int s = 0, c = 0;
-      if (e < a.E) {
-        s = a.offsets ? min(max(__ldcg(a.offsets + e), 0), a.M) : 0;
-        c = a.offsets ? max(min(__ldcg(a.offsets + e + 1), a.M) - s, 0) : a.M;
-        start[e] = s;
-        count[e] = c;
+      int lo = 0, hi = a.M;
+      if (a.offsets) {
+        lo = min(max(__ldcg(a.offsets + min(e, a.E)), top), a.M);
+        for (int o = 1; o < 32; o <<= 1) lo = max(lo, __shfl_up_sync(0xFFFFFFFFu, lo, o));
+        hi = max(lo, min(__ldcg(a.offsets + min(e + 1, a.E)), a.M));
+        top = __shfl_sync(0xFFFFFFFFu, hi, 31);
       }
+      const int c = e < a.E ? hi - lo : 0;
       int p = (c + a.NT - 1) / a.NT;
       for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xFFFFFFFFu, p, o);
         if (lane >= o) p += up;
       }
-      if (e < a.E) first[e + 1] = sum + p;
+      if (e < a.E) {
+        start[e] = lo;
+        count[e] = c;
+        first[e + 1] = sum + p;
+      }
       sum += __shfl_sync(0xFFFFFFFFu, p, 31);
     }
     if (lane == 0) first[0] = 0;
   }
   tc_fence_before();
-  __syncthreads();
+  if (kPair) {
+    cluster_sync();  // both CTAs' barriers exist before either signals the other
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  LinTiles tiles{first, start, count, a.E, a.nblk};
+  LinTiles tiles{first, start, count, a.E, a.tiles_n};
   const int total = tiles.total();
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producer
     uint32_t s = 0, p = 0, armed = 0, par = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    for (int tile = first_tile; tile < total; tile += tile_step) {
       const LinTile t = tiles.at(tile);
-      const int boxes = (t.n + kLinBoxRows - 1) / kLinBoxRows;
+      const int mine = t.n / kCtas;  // this CTA's rows of the codes
+      const int boxes = (mine + kLinBoxRows - 1) / kLinBoxRows;
       const uint32_t bytes = kLinATile + static_cast<uint32_t>(boxes) * (kLinBoxRows * 128u);
-      const int wrow = (t.e * a.nblk + t.nb) * a.Kb;
+      // the second CTA of the last pair may have no output block of its own: it reads the last one again
+      const int nb = min(t.nb * kCtas + static_cast<int>(rank), a.nblk - 1);
+      const int wrow = (t.e * a.nblk + nb) * a.Kb;
+      const int row = t.row0 + static_cast<int>(rank) * mine;
       for (int kb = 0; kb < a.Kb; ++kb) {
         if (!mbar_wait(empty + 8 * s, p ^ 1, abort_flag, limit, kErrTimeoutProducer)) goto producer_done;
         const uint32_t dst = base + s * a.stage_bytes;
-        mbar_arrive_expect_tx(full + 8 * s, bytes);
+        const uint32_t bar = full + 8 * s;
+        if (leader) mbar_arrive_expect_tx(bar, bytes * kCtas);
         if (check_bounds(bytes <= a.stage_bytes && wrow + kb < a.E * a.nblk * a.Kb && s < static_cast<uint32_t>(a.stages) &&
                          t.row0 >= 0 && t.row0 < a.M)) {
-          tma_load_2d(dst, &tmap_w, full + 8 * s, 0, (wrow + kb) * kFp8Block);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(dst + kLinATile + i * (kLinBoxRows * 128), &tmap_x, full + 8 * s, kb * kFp8Block,
-                        t.row0 + i * kLinBoxRows);
+          if (kPair) {
+            const uint32_t lead = map_to_cta(bar, 0);
+            tma_load_2d_pair(dst, &tmap_w, lead, 0, (wrow + kb) * kFp8Block);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d_pair(dst + kLinATile + i * (kLinBoxRows * 128), &tmap_x, lead, kb * kFp8Block,
+                               row + i * kLinBoxRows);
+          } else {
+            tma_load_2d(dst, &tmap_w, bar, 0, (wrow + kb) * kFp8Block);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(dst + kLinATile + i * (kLinBoxRows * 128), &tmap_x, bar, kb * kFp8Block,
+                          row + i * kLinBoxRows);
+          }
         }
         armed |= 1u << s;
         par = (par & ~(1u << s)) | (p << s);
@@ -394,51 +481,65 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     }
   producer_done:
-    if (*abort_flag) {
+    if (*abort_flag && leader) {
       // let every copy counted on this CTA's barriers land before it exits
       int dummy = 0;
       for (int i = 0; i < a.stages; ++i)
         if (armed >> i & 1) mbar_wait(full + 8 * i, par >> i & 1, &dummy, limit, kErrTimeoutDrain);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && leader) {
     // ---------------------------------------------------------- MMA issuer
     // The whole warp runs the loop; lane 0 waits, one elected lane issues.
-    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    auto wait = [&](uint32_t bar, uint32_t parity, bool cluster_scope) -> bool {
       int ok = 1;
-      if (lane == 0) ok = mbar_wait(bar, parity, abort_flag, limit, kErrTimeoutMma);
+      if (lane == 0)
+        ok = cluster_scope ? mbar_wait_cluster(bar, parity, abort_flag, limit, kErrTimeoutMma)
+                           : mbar_wait(bar, parity, abort_flag, limit, kErrTimeoutMma);
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       __syncwarp();
       tc_fence_after();
       return ok != 0;
     };
+    auto commit = [&](uint32_t bar) {
+      if (kPair) {
+        mma_commit_pair_multicast(bar, 0x3);
+      } else {
+        mma_commit(bar);
+      }
+    };
     uint32_t s = 0, p = 0, g = 0, gp = 0, c = 0, cp = 0;
     bool issued = false, ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+    for (int tile = first_tile; tile < total && ok; tile += tile_step) {
       const LinTile t = tiles.at(tile);
       const uint32_t d = tmem_base + c * a.acc_cols;
-      if (!check_bounds(static_cast<uint32_t>(t.n) <= a.acc_cols) || !(ok = wait(acc_empty + 8 * c, cp ^ 1))) {
+      if (!check_bounds(static_cast<uint32_t>(t.n) <= a.acc_cols) || !(ok = wait(acc_empty + 8 * c, cp ^ 1, kPair))) {
         ok = false;
         break;
       }
       for (int kb = 0; kb < a.Kb; ++kb) {
-        if ((kb & 3) == 0 && !(ok = wait(sf_full + 8 * g, gp))) break;
-        if (!(ok = wait(full + 8 * s, p))) break;
+        const bool last = kb == a.Kb - 1, group_end = (kb & 3) == 3 || last;
+        // (the scale words are written by threads of both CTAs of a pair)
+        if ((kb & 3) == 0 && !(ok = wait(sf_full + 8 * g, gp, kPair))) break;
+        if (!(ok = wait(full + 8 * s, p, false))) break;
         const uint32_t st = base + s * a.stage_bytes;
         const uint64_t ad = sw128_kmajor_desc(st, 1024u), bd = sw128_kmajor_desc(st + kLinATile, 1024u);
-        const uint32_t sf = tmem_base + a.sf_col + g * 8;
-        const uint32_t idesc = idesc_mxf8(128, static_cast<uint32_t>(t.n), static_cast<uint32_t>(kb & 3));
-        const int ks = kb == a.Kb - 1 ? a.last_ksteps : 4;
+        const uint32_t sf = tmem_base + a.sf_col + g * kLinSfCols<kPair>;
+        const uint32_t idesc = idesc_mxf8(128 * kCtas, static_cast<uint32_t>(t.n), static_cast<uint32_t>(kb & 3));
         if (elect_one()) {
-          for (int j = 0; j < ks; ++j)  // 32 bytes of K = 2 units of the descriptors
-            mma_mxf8(d, ad + 2 * j, bd + 2 * j, idesc, sf, sf + 4, (kb | j) != 0);
-          mma_commit(empty + 8 * s);
-          if ((kb & 3) == 3 || kb == a.Kb - 1) mma_commit(sf_empty + 8 * g);
-          if (kb == a.Kb - 1) mma_commit(acc_full + 8 * c);
+          const uint32_t acc = kb != 0;
+          with_ksteps(last ? static_cast<uint32_t>(a.last_ksteps) : 4u, [&](auto KS) {
+#pragma unroll
+            for (int j = 0; j < decltype(KS)::value; ++j)  // 32 bytes of K = 2 units of the descriptors
+              mma_mxf8<kPair>(d, ad + 2 * j, bd + 2 * j, idesc, sf, sf + 4, j == 0 ? acc : 1u);
+          });
+          commit(empty + 8 * s);
+          if (group_end) commit(sf_empty + 8 * g);
+          if (last) commit(acc_full + 8 * c);
         }
         __syncwarp();
         issued = true;
         if (++s == static_cast<uint32_t>(a.stages)) { s = 0; p ^= 1; }
-        if ((kb & 3) == 3 || kb == a.Kb - 1) {
+        if (group_end) {
           g ^= 1;
           gp ^= g == 0;
         }
@@ -449,26 +550,32 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (!ok && issued && lane == 0) {
       // the tensor cores finish what was issued before TMEM is freed
       int dummy = 0;
-      mma_commit(drain_bar);
+      if (kPair) {
+        mma_commit_pair(drain_bar);
+      } else {
+        mma_commit(drain_bar);
+      }
       mbar_wait(drain_bar, 0, &dummy, limit, kErrTimeoutDrain);
     }
     __syncwarp();
   } else if (warp >= 2 && warp < 2 + kLinScaleWarps) {
     // -------------------------------------------------------------- scales
     // Group of four blocks: the weights' word (the same for all 128 channels)
-    // into four columns, the rows' words into four: row 32 j + l at lane l of
-    // column j.
+    // into four columns, the rows' words into the next: row 32 j + l at lane l
+    // of column j.
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    constexpr int kRowCols = kLinSfCols<kPair> - 4;
     uint32_t g = 0, gp = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+    for (int tile = first_tile; tile < total && ok; tile += tile_step) {
       const LinTile t = tiles.at(tile);
-      const uint32_t* const ws = a.w_scale + static_cast<int64_t>(t.e * a.nblk + t.nb) * a.kgroups;
+      const int nb = min(t.nb * kCtas + static_cast<int>(rank), a.nblk - 1);
+      const uint32_t* const ws = a.w_scale + static_cast<int64_t>(t.e * a.nblk + nb) * a.kgroups;
       for (int kg = 0; kg < a.kgroups; ++kg) {
-        uint32_t w[8];
+        uint32_t w[4 + kRowCols];
         w[0] = w[1] = w[2] = w[3] = __ldcg(ws + kg);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kRowCols; ++j) {
           const int row = t.row0 + 32 * j + lane;
           w[4 + j] = 32 * j < t.n && row < a.M ? __ldcg(a.x_scale + static_cast<int64_t>(kg) * a.M + row) : 0x7F7F7F7Fu;
         }
@@ -477,45 +584,105 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (!(ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0)) break;
         __syncwarp();
         tc_fence_after();
-        const uint32_t dst = tmem_base + quarter + a.sf_col + g * 8;
-        tmem_st_x4(dst, w);
-        tmem_st_x4(dst + 4, w + 4);
+        const uint32_t dst = tmem_base + quarter + a.sf_col + g * kLinSfCols<kPair>;
+#pragma unroll
+        for (int j = 0; j < 4 + kRowCols; j += 4) tmem_st_x4(dst + j, w + j);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sf_full + 8 * g);
+        if (lane == 0) {
+          if (kPair) {
+            mbar_arrive_cluster(map_to_cta(sf_full + 8 * g, 0));
+          } else {
+            mbar_arrive(sf_full + 8 * g);
+          }
+        }
         g ^= 1;
         gp ^= g == 0;
       }
     }
   } else if (warp >= 2 + kLinScaleWarps) {
     // ------------------------------------------------------------ epilogue
+    // 32 rows of x (columns) by this warp's 32 channels (lanes) at a time:
+    // sums + bias, rounded to bf16, transposed through shared memory (64-byte
+    // lines of 32 channels, 16-byte groups permuted by the line against bank
+    // conflicts) and written as 16-byte groups of 8 channels.
     const int q = warp & 3;
+    const uint32_t buf = epi_stage + static_cast<uint32_t>(warp - 2 - kLinScaleWarps) * kLinEpiBuf;
+    const uint32_t empty_leader = kPair ? map_to_cta(acc_empty, 0) : acc_empty;
+    // stmatrix: lane 8 i + j gives line 8 * step + j, group i
+    const uint32_t st_line = static_cast<uint32_t>(lane & 7), st_grp = static_cast<uint32_t>(lane >> 3);
+    const uint32_t st_addr = buf + st_line * 64u + ((st_grp ^ (st_line >> 1)) << 4);
+    // reading back: lane 4 j + i reads line 8 * step + j, group i
+    const uint32_t ld_line = static_cast<uint32_t>(lane >> 2), ld_grp = static_cast<uint32_t>(lane & 3);
+    const uint32_t ld_addr = buf + ld_line * 64u + ((ld_grp ^ ((ld_line >> 1) & 3u)) << 4);
     uint32_t c = 0, cp = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    for (int tile = first_tile; tile < total; tile += tile_step) {
       const LinTile t = tiles.at(tile);
+      const int ch0 = (t.nb * kCtas + static_cast<int>(rank)) * kFp8Block + q * 32;  // this warp's first channel
+      float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // bias of channels ch0 + 8 i + lane / 4
+      if (a.bias) {
+        const __nv_bfloat16* const be = a.bias + static_cast<int64_t>(t.e) * a.N;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (ch0 + 8 * i + (lane >> 2) < a.N) b[i] = __bfloat162float(be[ch0 + 8 * i + (lane >> 2)]);
+      }
       int got = 1;
       if (lane == 0) got = mbar_wait(acc_full + 8 * c, cp, abort_flag, limit, kErrTimeoutEpilogue);
       if (!__shfl_sync(0xFFFFFFFFu, got, 0)) break;
       __syncwarp();
       tc_fence_after();
-      const int ch = t.nb * kFp8Block + q * 32 + lane;
-      const float b = a.bias && ch < a.N ? __bfloat162float(a.bias[static_cast<int64_t>(t.e) * a.N + ch]) : 0.0f;
       const uint32_t src = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c * a.acc_cols;
+      const int ch = ch0 + 8 * static_cast<int>(ld_grp);  // the group of channels this lane writes
       for (int r0 = 0; r0 < t.rows; r0 += 32) {
         uint32_t v[32];
-        tmem_ld_32x32b_x32(src + static_cast<uint32_t>(r0), v);
+        tmem_ld_16x256b_x4(src + static_cast<uint32_t>(r0), v);
+        tmem_ld_16x256b_x4(src + (16u << 16) + static_cast<uint32_t>(r0), v + 16);
         tmem_ld_wait(v);
-        if (ch < a.N) {
-          __nv_bfloat16* dst = a.out + (t.row0 + r0) * a.ldo + ch;
+        __syncwarp();  // the last block's lines have been read
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (r0 + j < t.rows && check_bounds(t.row0 + r0 + j < a.M)) dst[j * a.ldo] = __float2bfloat16_rn(__uint_as_float(v[j]) + b);
+        for (int step = 0; step < 4; ++step) {  // 8 rows of x: matrices of channels 0-7, 8-15, 16-23, 24-31
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = (i >> 1) * 16 + step * 4 + (i & 1) * 2;
+            const __nv_bfloat162 p2 =
+                __floats2bfloat162_rn(__uint_as_float(v[at]) + b[i], __uint_as_float(v[at + 1]) + b[i]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p2);
+          }
+          stmatrix_x4_trans(st_addr + static_cast<uint32_t>(step) * 512u, w);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int step = 0; step < 4; ++step) {
+          const int r = r0 + step * 8 + static_cast<int>(ld_line);
+          if (r < t.rows && ch < a.N && check_bounds(t.row0 + r < a.M)) {
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(ld_addr + static_cast<uint32_t>(step) * 512u));
+            __nv_bfloat16* const dst = a.out + (t.row0 + r) * a.ldo + ch;
+            if (a.vec_out && ch + 8 <= a.N) {
+              *reinterpret_cast<uint4*>(dst) = w;
+            } else {
+              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (ch + i < a.N)
+                  reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(u[i >> 1] >> ((i & 1) * 16));
+            }
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty + 8 * c);
+      if (lane == 0) {
+        if (kPair) {
+          mbar_arrive_remote(empty_leader + 8 * c);
+        } else {
+          mbar_arrive(acc_empty + 8 * c);
+        }
+      }
       c ^= 1;
       cp ^= c == 0;
     }
@@ -523,11 +690,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if (kPair) {
+    cluster_sync();  // neither CTA leaves while its partner may still touch its memory
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    tmem_dealloc(tmem_base, a.tmem_cols);
+    if (kPair) {
+      tmem_dealloc_pair(tmem_base, a.tmem_cols);
+    } else {
+      tmem_dealloc(tmem_base, a.tmem_cols);
+    }
   }
 }
 

@@ -308,6 +308,27 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, int block, siz
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// How many CTA pairs of a kernel with all of an SM's shared memory the device holds at once (kept in *known).
+template <typename Kernel>
+int max_pairs(Kernel kernel, int threads, int sms, int* known) {
+  if (*known) return QVAE_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * sms);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = kSmemLimit;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  QVAE_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg));
+  *known = std::max(n, 1);
+  return QVAE_OK;
+}
+
 // carry: xq holds T + 2 frames per batch item, the first two carried from
 // the previous chunk of a streamed video (output frames are the last T).
 // halo_top / halo_bot: xq holds H + halo_top + halo_bot rows, output row h
@@ -465,22 +486,7 @@ int launch_conv(const qvae_shape* shape, const void* xq, const float* x_scale,
   int grid;
   if (t.pair) {
     int& max_clusters = g_max_clusters[dev][fuse ? 1 : 0];
-    if (max_clusters == 0) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2 * sms);
-      cfg.blockDim = dim3(threads);
-      cfg.dynamicSmemBytes = kSmemLimit;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      int n = 0;
-      QVAE_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg));
-      max_clusters = std::max(n, 1);
-    }
+    if ((rc = max_pairs(kernel, threads, sms, &max_clusters))) return rc;
     const int cta_limit = g_cta_limit.load();
     int clusters = std::min(t.num_tiles, max_clusters);
     if (cta_limit > 0) clusters = std::max(1, std::min(clusters, cta_limit / 2));
@@ -577,7 +583,51 @@ int launch_quant_from_amax(const void* x, int64_t numel, const uint32_t* amax, i
 constexpr int64_t kLinMaxRows = int64_t{1} << 30;      // rows of x in a call
 constexpr int64_t kLinMaxChannels = int64_t{1} << 20;  // N, K
 
-bool g_lin_attr_set[kMaxDevices] = {};
+std::atomic<int32_t> g_lin_force[3] = {};  // NT, mode (1 single CTA, 2 CTA pair), cap on the CTAs; 0 = automatic
+bool g_lin_attr_set[kMaxDevices][2] = {};
+int g_lin_max_clusters[kMaxDevices] = {0};
+
+// How a product is tiled.
+struct LinPlan {
+  bool pair;
+  int NT;             // most rows of a tile
+  int64_t max_tiles;  // tiles of any offsets
+};
+
+// Tiles of `nt` rows by one or two output blocks: what the rows give at most (each expert may end in a tile of its own).
+int64_t linear_tiles(int64_t E, int64_t M, int64_t nblk, bool grouped, bool pair, int nt) {
+  const int64_t spans = ceil_div(M, nt) + (grouped ? std::min(E, M) - (M > 0 ? 1 : 0) : 0);
+  return spans * (pair ? ceil_div(nblk, 2) : nblk);
+}
+
+// The tiling with the least estimated time.  A launch takes waves of tiles, one to an SM (to two SMs: a CTA pair); a
+// tile takes Kb * 4 MMAs and what its epilogue leaves exposed.
+LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms) {
+  const int64_t nblk = ceil_div(N, qvae::kFp8Block), Kb = ceil_div(K, qvae::kFp8Block);
+  const int64_t busy = grouped ? std::min(E, M) : 1;     // experts that have rows, at most
+  const double rows = static_cast<double>(M) / busy;     // of one of them
+  LinPlan best = {};
+  double least = 0;
+  for (int mode = 1; mode <= 2; ++mode) {
+    if (g_lin_force[1] && mode != g_lin_force[1]) continue;
+    const bool pair = mode == 2;
+    const int most = pair ? qvae::kLinMaxNT<true> : qvae::kLinMaxNT<false>;
+    for (int nt = 16; nt <= most; nt += 16) {
+      if (g_lin_force[0] && nt != std::min<int>(g_lin_force[0], most)) continue;
+      const double spans = busy * std::ceil(rows / nt);
+      const double tiles = spans * (pair ? ceil_div(nblk, 2) : nblk);
+      const double n = std::min<double>(nt, std::ceil(rows / std::ceil(rows / nt) / 16) * 16);
+      const double mma = pair ? std::max(72.0, 0.56 * n) : std::max(64.0, 0.8 * n);
+      const double tile = Kb * 4 * mma + 600.0 + (pair ? 4.0 : 4.0) * n;
+      const double time = std::ceil(tiles / (pair ? sms / 2 : sms)) * tile;
+      if (!best.NT || time < least) {
+        best = {pair, nt, linear_tiles(E, M, nblk, grouped, pair, nt)};
+        least = time;
+      }
+    }
+  }
+  return best;
+}
 
 int check_linear(int64_t E, int64_t M, int64_t N, int64_t K) {
   if (E < 0 || M < 0 || N < 0 || K < 0) return QVAE_ERR_ARG;
@@ -640,19 +690,26 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.last_ksteps = static_cast<int>(ceil_div(K - int64_t{a.Kb - 1} * qvae::kFp8Block, 32));
   a.nblk = static_cast<int>(ceil_div(N, qvae::kFp8Block));
   a.kgroups = (a.Kb + 3) / 4;
-  const int64_t rows = ceil_div(M, E);  // of an expert, on average
-  a.NT = static_cast<int>(std::min<int64_t>(qvae::kLinMaxNT, ceil_div(rows, 16) * 16));
-  if ((ceil_div(M, a.NT) + E) * a.nblk > INT32_MAX / 2) return QVAE_ERR_SHAPE;
-  const int box_rows = (a.NT + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
+  const LinPlan plan = plan_linear(E, M, N, K, offsets != nullptr, sms);
+  if (plan.max_tiles > INT32_MAX / 2) return QVAE_ERR_SHAPE;
+  const int ctas = plan.pair ? 2 : 1;
+  a.NT = plan.NT;
+  a.tiles_n = (a.nblk + ctas - 1) / ctas;
+  // a CTA's part of a tile's rows, in whole boxes
+  const int box_rows = (a.NT / ctas + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
   a.stage_bytes = qvae::kLinATile + static_cast<uint32_t>(box_rows) * 128u;
-  const uint32_t rest = 1024u + qvae::kLinBars + 8u + 4u * static_cast<uint32_t>(3 * E + 1);
+  const uint32_t rest = 1024u + qvae::kLinEpiWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u +
+                        4u * static_cast<uint32_t>(3 * E + 1);
   a.stages = std::min<int>(qvae::kLinMaxStages, (kSmemLimit - rest) / a.stage_bytes);
   const uint32_t smem = rest + a.stages * a.stage_bytes;
   // two accumulators (the epilogue reads 32 columns at a time) and two sets of scale words
+  const uint32_t sf_cols = plan.pair ? qvae::kLinSfCols<true> : qvae::kLinSfCols<false>;
   a.acc_cols = static_cast<uint32_t>(a.NT);
-  a.sf_col = a.acc_cols + static_cast<uint32_t>(box_rows);
+  a.sf_col = 2 * a.acc_cols;
+  const uint32_t cols = std::max(a.sf_col + 2 * sf_cols, a.acc_cols + (a.acc_cols + 31) / 32 * 32);
   a.tmem_cols = 32;
-  while (a.tmem_cols < a.sf_col + 16) a.tmem_cols <<= 1;
+  while (a.tmem_cols < cols) a.tmem_cols <<= 1;
+  a.vec_out = aligned16(out) && (ldo % 8 == 0 || M == 1);
   a.offsets = offsets;
   a.x_scale = x_scale;
   a.w_scale = reinterpret_cast<const uint32_t*>(w_scale);
@@ -676,13 +733,19 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     if ((rc = encode_map(&tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, dims, strides, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE)))
       return rc;
   }
-  if (!g_lin_attr_set[dev]) {
-    QVAE_CUDA(cudaFuncSetAttribute(qvae::linear_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
-    g_lin_attr_set[dev] = true;
+  const auto kernel = plan.pair ? qvae::linear_fp8_kernel<true> : qvae::linear_fp8_kernel<false>;
+  if (!g_lin_attr_set[dev][plan.pair]) {
+    QVAE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
+    g_lin_attr_set[dev][plan.pair] = true;
   }
-  const int64_t most_tiles = (offsets ? ceil_div(M, a.NT) + std::min(E, M) : ceil_div(M, a.NT)) * a.nblk;
-  const int grid = static_cast<int>(std::min<int64_t>(most_tiles, sms));
-  QVAE_CUDA(launch_dependent(qvae::linear_fp8_kernel, dim3(grid), qvae::kLinThreads, smem, stream, 1, tmap_x, tmap_w, a));
+  int grid = sms;
+  if (plan.pair) {
+    if ((rc = max_pairs(kernel, qvae::kLinThreads, sms, &g_lin_max_clusters[dev]))) return rc;
+    grid = 2 * g_lin_max_clusters[dev];
+  }
+  if (const int cap = g_lin_force[2]) grid = std::min(grid, cap);
+  grid = static_cast<int>(std::min<int64_t>(plan.max_tiles * ctas, std::max(grid / ctas, 1) * ctas));
+  QVAE_CUDA(launch_dependent(kernel, dim3(grid), qvae::kLinThreads, smem, stream, ctas, tmap_x, tmap_w, a));
   return QVAE_OK;
 }
 
@@ -1201,6 +1264,28 @@ int qvae_set_conv_tiling(int32_t MS, int32_t NT, int32_t SA, int32_t SB, int32_t
 int qvae_set_fused_quant(int32_t on) {
   if (on < 0 || on > 1) return QVAE_ERR_ARG;
   g_fused_quant = on != 0;
+  return QVAE_OK;
+}
+
+int qvae_set_linear_tiling(int32_t NT, int32_t mode, int32_t max_ctas) {
+  if (NT < 0 || NT > qvae::kLinMaxNT<true> || NT % 16 || mode < 0 || mode > 2 || max_ctas < 0) return QVAE_ERR_ARG;
+  g_lin_force[0] = NT;
+  g_lin_force[1] = mode;
+  g_lin_force[2] = max_ctas;
+  return QVAE_OK;
+}
+
+int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* out2) {
+  if (!out2) return QVAE_ERR_ARG;
+  const int rc = check_linear(std::max(E, 1), M, N, K);
+  if (rc) return rc;
+  if (E < 0) return QVAE_ERR_ARG;
+  int sms = 148, dev;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) sm_count(dev, &sms);
+  cudaGetLastError();
+  const LinPlan plan = plan_linear(std::max(E, 1), std::max<int64_t>(M, 1), N, K, E > 0, sms);
+  out2[0] = plan.NT;
+  out2[1] = plan.pair ? 2 : 1;
   return QVAE_OK;
 }
 
