@@ -405,7 +405,7 @@ size_t qvae_fp8_weight_scale_bytes(int32_t E, int32_t N, int32_t K);
 int qvae_fp8_quantize_weights(int32_t E, int32_t N, int32_t K, const void* w_bf16, uint8_t* wq_packed,
                               uint8_t* w_scale, void* stream);
 
-/* Bytes of the codes (M rows of 128 * ceil(K/128)) and scales (M * ceil(K/512) words) of M rows,
+/* Bytes of the codes (ceil(K/128) blocks of M rows of 128) and scales (M * ceil(K/512) words) of M rows,
  * and of a workspace that holds both (the _fused entry points); 0 for sizes out of range. */
 size_t qvae_fp8_code_bytes(int64_t M, int32_t K);
 size_t qvae_fp8_scale_bytes(int64_t M, int32_t K);
@@ -415,7 +415,7 @@ size_t qvae_fp8_workspace_bytes(int64_t M, int32_t K);
  * Dynamic activation quantisation of M rows.
  *   op        qvae_fp8_op: what is quantised.
  *   x_bf16    rows of K (QVAE_FP8_SILU_MUL: 2 K) bf16 values, ldx elements apart.
- *   xq        [M][128 * ceil(K/128)] codes, written; zeros beyond K.
+ *   xq        [ceil(K/128)][M][128] codes, written; zeros beyond K.
  *   x_scale   [ceil(K/512)][M] words, written: byte j of word (g, m) is the
  *             scale of row m's block 4 g + j (1 beyond the last block).
  */

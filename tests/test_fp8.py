@@ -145,7 +145,7 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
     with pytest.raises(ValueError):
         qvae.linear_fp8_fused(x, w)
     with pytest.raises(ValueError):
-        qvae.linear_fp8(torch.zeros((4, 128), dtype=torch.uint8), torch.zeros((1, 4), dtype=torch.int32), w)
+        qvae.linear_fp8(torch.zeros((1, 4, 128), dtype=torch.uint8), torch.zeros((1, 4), dtype=torch.int32), w)
 
 
 def test_binding_checks_of_layouts():

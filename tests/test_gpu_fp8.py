@@ -50,6 +50,11 @@ def plain_bits(codes):
     return torch.where(b == 0x80, torch.zeros_like(b), b)
 
 
+def by_row(codes):
+    """[M, 128 kb] of codes [kb, M, 128]."""
+    return codes.permute(1, 0, 2).reshape(codes.shape[1], -1)
+
+
 def scale_bytes(words, kb):
     """[M, kb] bytes of scale words [kg, M]."""
     m = words.shape[1]
@@ -87,7 +92,7 @@ def test_activation_codes_and_scales_are_exact(q, m, k, extra):
     codes, words = q.fp8_quant_act(x)
     want, byte = ref.quantise(x, 1)
     assert torch.equal(scale_bytes(words, byte.shape[1]).long(), byte)
-    assert torch.equal(plain_bits(codes), code_bits(want))
+    assert torch.equal(plain_bits(by_row(codes)), code_bits(want))
     assert (scale_bytes(words, words.shape[0] * 4)[:, byte.shape[1]:] == 1).all()
     assert q.qvae_get_error() == 0
 
@@ -100,7 +105,7 @@ def test_activation_codes_of_every_bf16_value(q):
         codes, words = q.fp8_quant_act(y.contiguous())
         want, byte = ref.quantise(y, 1)
         assert torch.equal(scale_bytes(words, byte.shape[1]).long(), byte)
-        assert torch.equal(plain_bits(codes), code_bits(want))
+        assert torch.equal(plain_bits(by_row(codes)), code_bits(want))
 
 
 def test_activation_groups_with_infinities_and_nan(q):
@@ -111,7 +116,7 @@ def test_activation_groups_with_infinities_and_nan(q):
     assert (byte == 255).sum() == 3
     assert torch.equal(scale_bytes(words, 3).long(), byte)
     # the group's codes are NaN, the padding of its last block included
-    assert torch.equal(plain_bits(codes), code_bits(want))
+    assert torch.equal(plain_bits(by_row(codes)), code_bits(want))
 
 
 @pytest.mark.parametrize("m,k,extra", [(1, 1, 0), (4, 129, 0), (65, 1024, 16), (9, 1000, 0), (40, 333, 5)])
@@ -129,7 +134,7 @@ def test_activation_codes_of_silu_mul(q, m, k, extra):
     rel = (h[:, :k].double().abs() + 4) * 2.0 ** -22
     scale = torch.exp2(byte.double() - 127)
     assert ((amax * (1 - 2.0 ** -14) <= 448 * scale) & ((byte == 1) | (amax * (1 + 2.0 ** -14) > 224 * scale))).all()
-    got = codes.view(torch.float8_e4m3fn).double().view(m, -1, 128) * scale[:, :, None]
+    got = by_row(codes).view(torch.float8_e4m3fn).double().view(m, -1, 128) * scale[:, :, None]
     got = got.view(m, -1)
     assert (got[:, k:] == 0).all()
     s = scale.repeat_interleave(128, 1)[:, :k]

@@ -695,9 +695,8 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   const int ctas = plan.pair ? 2 : 1;
   a.NT = plan.NT;
   a.tiles_n = (a.nblk + ctas - 1) / ctas;
-  // a CTA's part of a tile's rows, in whole boxes
-  const int box_rows = (a.NT / ctas + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
-  a.stage_bytes = qvae::kLinATile + static_cast<uint32_t>(box_rows) * 128u;
+  a.box_rows = (a.NT / ctas + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
+  a.stage_bytes = qvae::kLinStageBlocks * (qvae::kLinATile + static_cast<uint32_t>(a.box_rows) * 128u);
   const uint32_t rest = 1024u + qvae::kLinEpiWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u +
                         4u * static_cast<uint32_t>(3 * E + 1);
   a.stages = std::min<int>(qvae::kLinMaxStages, (kSmemLimit - rest) / a.stage_bytes);
@@ -718,18 +717,20 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.ldo = ldo;
   a.wait_limit_ns = g_wait_limit_ns;
 
-  CUtensorMap tmap_x, tmap_w;
+  CUtensorMap tmap_x, tmap_xs, tmap_w;
   {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.Kb) * 128u, static_cast<cuuint64_t>(M)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.Kb) * 128u};
-    const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(qvae::kLinBoxRows)};
-    if ((rc = encode_map(&tmap_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, dims, strides, box, 2, CU_TENSOR_MAP_SWIZZLE_128B)))
+    const cuuint64_t dims[3] = {128u, static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(a.Kb)};
+    const cuuint64_t strides[2] = {128u, static_cast<cuuint64_t>(M) * 128u};
+    const cuuint32_t box[3] = {128u, static_cast<cuuint32_t>(a.box_rows), qvae::kLinStageBlocks};
+    const cuuint32_t small[3] = {128u, qvae::kLinBoxRows, 1u};
+    if ((rc = encode_map(&tmap_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, dims, strides, box, 3, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+        (rc = encode_map(&tmap_xs, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, dims, strides, small, 3, CU_TENSOR_MAP_SWIZZLE_128B)))
       return rc;
   }
   {
     const cuuint64_t dims[2] = {128u, static_cast<cuuint64_t>(E) * a.nblk * a.Kb * qvae::kFp8Block};
     const cuuint64_t strides[1] = {128u};
-    const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(qvae::kFp8Block)};
+    const cuuint32_t box[2] = {128u, qvae::kLinStageBlocks * qvae::kFp8Block};
     if ((rc = encode_map(&tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, dims, strides, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE)))
       return rc;
   }
@@ -745,7 +746,8 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   }
   if (const int cap = g_lin_force[2]) grid = std::min(grid, cap);
   grid = static_cast<int>(std::min<int64_t>(plan.max_tiles * ctas, std::max(grid / ctas, 1) * ctas));
-  QVAE_CUDA(launch_dependent(kernel, dim3(grid), qvae::kLinThreads, smem, stream, ctas, tmap_x, tmap_w, a));
+  QVAE_CUDA(launch_dependent(kernel, dim3(grid), qvae::kLinThreads, smem, stream, ctas, tmap_x, tmap_xs, tmap_w,
+                             a));
   return QVAE_OK;
 }
 

@@ -535,7 +535,7 @@ def fp8_workspace(M: int, K: int, device="cuda") -> torch.Tensor:
 
 
 def fp8_quant_act(x: torch.Tensor, silu_mul: bool = False, stream=None):
-    """Codes (uint8 [M, 128 ceil(K/128)]) and scale words (int32 [ceil(K/512), M]) of bf16 rows x [M, K]
+    """Codes (uint8 [ceil(K/128), M, 128]) and scale words (int32 [ceil(K/512), M]) of bf16 rows x [M, K]
     (silu_mul: [M, 2 K], of which silu(x[:, :K]) * x[:, K:] is quantised)."""
     device = _cuda(x, "x")
     _want(x.dim() == 2 and x.shape[1] >= 1 and not (silu_mul and x.shape[1] % 2),
@@ -545,7 +545,7 @@ def fp8_quant_act(x: torch.Tensor, silu_mul: bool = False, stream=None):
     ld = _row_stride(x, columns, device, "x")
     ctx, handle = _on_stream(device, stream)
     with ctx:
-        xq = torch.empty((M, -(-K // 128) * 128), dtype=torch.uint8, device=device)
+        xq = torch.empty((-(-K // 128), M, 128), dtype=torch.uint8, device=device)
         xs = torch.empty((-(-K // 512), M), dtype=torch.int32, device=device)
         _check("qvae_fp8_quant_act",
                lib().qvae_fp8_quant_act(M, K, QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN, x.data_ptr(), ld,
@@ -576,11 +576,12 @@ def _layer(device, weights, M, bias, out, offsets):
 
 def _product(name, xq, x_scale, weights, bias, out, offsets, stream):
     device = _cuda(xq, "xq")
-    M = xq.shape[0]
     K = weights.K
-    px = _buffer(xq, torch.uint8, M * -(-K // 128) * 128, device, "xq")
+    _want(xq.dim() == 3 and xq.shape[0] == -(-K // 128) and xq.shape[2] == 128,
+          f"xq: codes [{-(-K // 128)}, rows, 128] of {K} input channels are needed")
+    M = xq.shape[1]
+    px = _buffer(xq, torch.uint8, xq.numel(), device, "xq")
     ps = _buffer(x_scale, torch.int32, M * -(-K // 512), device, "x_scale")
-    _want(xq.dim() == 2 and xq.shape[1] == -(-K // 128) * 128, f"xq: codes of {K} input channels are needed")
     ldo, pw, pws, pb, po = _layer(device, weights, M, bias, out, offsets)
     ctx, handle = _on_stream(device, stream)
     with ctx:
