@@ -139,10 +139,10 @@ def test_activation_codes_of_silu_mul(q, m, k, extra):
     assert (got[:, k:] == 0).all()
     s = scale.repeat_interleave(128, 1)[:, :k]
     half = torch.exp2(torch.floor(torch.log2(torch.clamp(v.abs() / s, min=2.0 ** -6))) - 4) * s
-    # a value below a power of two may be rounded on the finer or the coarser side of it.  Where exp(-gate) is beyond
-    # fp32 (gate < -88.72 = ln 2^-128) the fp32 form gives 0; what it should give is at most
-    # |gate| exp(gate) |up| <= 88.72 * 2^-128 |up| < 2^-121 |up| there (x exp(-x) falls for x > 1)
-    lost = torch.where(h[:, :k] < -88.5, 2.0 ** -121, 0.0) * h[:, k:2 * k].double().abs()
+    # a value below a power of two may be rounded on the finer or the coarser side of it.  Where 1 + exp(-gate) is
+    # above 2^126 (gate < -87.33) its reciprocal is below fp32's normal numbers and counts as 0; what is lost is at most
+    # |gate| exp(gate) |up| <= 87.33 * 2^-126 |up| < 2^-119 |up| there (x exp(-x) falls for x > 1)
+    lost = torch.where(h[:, :k] < -87.3, 2.0 ** -119, 0.0) * h[:, k:2 * k].double().abs()
     assert bool(((got[:, :k] - v).abs() <= half * (1 + 2.0 ** -8) + rel * v.abs() + 2.0 ** -149 + lost).all())
 
 

@@ -658,7 +658,9 @@ int launch_fp8_quant(int64_t M, int64_t K, int op, const void* x, int64_t ldx, u
   using Kernel = void (*)(const uint16_t*, int64_t, int, int, int, uint8_t*, uint32_t*);
   const Kernel kernels[4] = {qvae::fp8_quant_act_kernel<false, false>, qvae::fp8_quant_act_kernel<false, true>,
                              qvae::fp8_quant_act_kernel<true, false>, qvae::fp8_quant_act_kernel<true, true>};
-  const dim3 grid(static_cast<unsigned>(ceil_div(M, qvae::kFp8RowsPerBlock)), static_cast<unsigned>(ceil_div(Kb, 4)));
+  const int64_t blocks = ceil_div(M, silu ? qvae::kFp8RowsPerBlock<true> : qvae::kFp8RowsPerBlock<false>) * ceil_div(Kb, 4);
+  if (blocks > INT32_MAX) return QVAE_ERR_SHAPE;
+  const dim3 grid(static_cast<unsigned>(blocks));
   QVAE_CUDA(launch_dependent(kernels[(silu ? 2 : 0) + (vec ? 1 : 0)], grid, qvae::kFp8QuantThreads, 0, stream, 1,
                              static_cast<const uint16_t*>(x), ldx, static_cast<int>(M), static_cast<int>(K), Kb, xq,
                              x_scale));
