@@ -523,14 +523,18 @@ int qvae_set_conv_cta_limit(int32_t max_ctas);
  * 256 of a CTA pair.
  *   NT        a multiple of 16, <= 240 (single CTAs take at most 128)
  *   mode      1 = single CTAs, 2 = CTA pairs (cta_group::2)
- *   max_ctas  cap on the CTAs of a launch
- * Zero = automatic.
+ *   split     CTAs that share a tile along K, <= 8 (single CTAs; as many as
+ *             there are pairs of 128-channel blocks at most, and only where all
+ *             tiles' CTAs fit the device twice)
+ *   max_ctas  cap on the CTAs of a launch (split 1)
+ * Zero = automatic.  A forced value that a call's sizes do not allow is taken
+ * as automatic for that call.
  */
-int qvae_set_linear_tiling(int32_t NT, int32_t mode, int32_t max_ctas);
+int qvae_set_linear_tiling(int32_t NT, int32_t mode, int32_t split, int32_t max_ctas);
 
-/* The tiling that a product of these sizes would use: out[0] = NT, out[1] =
- * mode.  E = 0: a single layer; else grouped by E experts. */
-int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* out2);
+/* The tiling that a product of these sizes would use: out[0..2] = NT, mode,
+ * split.  E = 0: a single layer; else grouped by E experts. */
+int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* out3);
 
 /*
  * How qvae_decode_layers runs quantised layers (process-wide, tuning and

@@ -496,7 +496,7 @@ def test_every_tiling_gives_the_same_products(q, mode, nt, ctas):
     if mode == 1 and nt > 128:
         pytest.skip("single CTAs take at most 128 rows")
     try:
-        q.qvae_set_linear_tiling(nt, mode, ctas)
+        q.qvae_set_linear_tiling(nt, mode, 1, ctas)
         for m, n, k in ((1, 128, 128), (37, 300, 700), (300, 129, 1100), (500, 520, 96)):
             x, w, b = rows(m, k, m), matrix((n, k), n), matrix((1, n), 3)[0]
             out = q.linear_fp8_fused(x, q.fp8_quantize_weights(w), b)
@@ -514,5 +514,35 @@ def test_every_tiling_gives_the_same_products(q, mode, nt, ctas):
             if counts[i]:
                 y, s = ref.linear(ref.act_values(x[o[i]:o[i + 1]]), ref.weight_values(w[i]))
                 check_product(out[o[i]:o[i + 1]], y, s, 600)
+    finally:
+        q.qvae_set_linear_tiling()
+
+
+@pytest.mark.parametrize("split", [2, 3, 5, 8])
+@pytest.mark.parametrize("nt", [16, 64, 128])
+def test_tiles_split_along_k(q, nt, split):
+    try:
+        q.qvae_set_linear_tiling(nt, 1, split)
+        for m, n, k in ((1, 128, 2048), (1, 300, 4096), (16, 257, 1100), (37, 300, 2000), (100, 129, 4444)):
+            x, w, b = rows(m, k, m), matrix((n, k), n), matrix((1, n), 3)[0]
+            p = q.fp8_quantize_weights(w)
+            out = q.linear_fp8_fused(x, p, b)
+            assert q.qvae_get_error() == 0
+            y, s = ref.linear(ref.act_values(x), ref.weight_values(w), b)
+            check_product(out, y, s, k)
+            assert torch.equal(out, q.linear_fp8_fused(x, p, b))      # the same bits every time
+            odd = torch.empty((m, n + 3), dtype=torch.bfloat16, device="cuda")[:, 1:n + 1]
+            assert torch.equal(out, q.linear_fp8_fused(x, p, b, out=odd))
+        counts = [3, 0, 1, 17, 0, 20]
+        o = spans(counts, 3)
+        x, w = rows(o[-1] + 2, 2100, 1), matrix((6, 300, 2100), 2)
+        out = torch.full((o[-1] + 2, 300), 3.25, dtype=torch.bfloat16, device="cuda")
+        q.linear_fp8_grouped_fused(x, torch.tensor(o, dtype=torch.int32, device="cuda"), q.fp8_quantize_weights(w), out=out)
+        assert q.qvae_get_error() == 0
+        assert (out[:3] == 3.25).all() and (out[o[-1]:] == 3.25).all()
+        for i in range(6):
+            if counts[i]:
+                y, s = ref.linear(ref.act_values(x[o[i]:o[i + 1]]), ref.weight_values(w[i]))
+                check_product(out[o[i]:o[i + 1]], y, s, 2100)
     finally:
         q.qvae_set_linear_tiling()

@@ -268,6 +268,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
   }
 }
 
+// Eight bf16 values, or the first `left` of them; vec: dst is on 16 bytes.
+__device__ __forceinline__ void store_bf16x8(__nv_bfloat16* dst, const uint4& w, int left, bool vec) {
+  if (vec && left >= 8) {
+    *reinterpret_cast<uint4*>(dst) = w;
+  } else {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(u[i >> 1] >> ((i & 1) * 16));
+  }
+}
+
 // Instruction descriptor of kind::mxf8f6f4: e4m3 x e4m3, both operands K-major, E8M0 scales,
 // byte `sf` of the scale words of both operands.
 __device__ __forceinline__ uint32_t idesc_mxf8(uint32_t M, uint32_t N, uint32_t sf) {
@@ -317,6 +329,8 @@ struct LinArgs {
   int stages;
   uint32_t stage_bytes;  // per 128-channel block of a stage: 16 KB of weights + box_rows rows of codes
   uint32_t acc_cols, sf_col, tmem_cols;
+  int split;             // CTAs of a cluster that share a tile along K (1, or one tile to a cluster; single CTAs)
+  int early;             // weights and offsets are final before the kernel before this one ends
   int vec_out;           // rows of out start on 16 bytes
   const int32_t* offsets;    // [E + 1] row offsets of the experts, or null (one span of M rows)
   const uint32_t* x_scale;   // [kgroups][M]
@@ -401,6 +415,16 @@ struct LinTiles {
 // the rows' codes, and writes the outputs of its own channels.  The leader
 // issues the MMAs; loads and scale words of both are counted on its barriers,
 // and its commits arrive on the barriers of both.
+//
+// Split along K (single CTAs): where few rows leave too few tiles to read the
+// weights with every SM, a cluster of `split` CTAs takes one tile, each a part
+// of its K.  The sums of each are put in its shared memory, added in the order
+// of the ranks over distributed shared memory (no atomics: the same bits every
+// time, and no workspace), and written.
+//
+// Launched as a programmatic dependent.  With `early` (the quantiser of the
+// same call in front) the first weights are loaded before its end is waited
+// for; codes, scales and everything written wait for it.
 template <bool kPair>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_xs,
@@ -427,8 +451,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   constexpr int kCtas = kPair ? 2 : 1;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;  // 0 = leader of the pair
   const bool leader = rank == 0;
-  const int first_tile = kPair ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
-  const int tile_step = kPair ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  const bool split = !kPair && a.split > 1;
+  const int first_tile = kPair || split ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int tile_step = kPair || split ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  // this CTA's blocks of K: whole stages
+  int kb0 = 0, kb1 = a.Kb;
+  if (split) {
+    const int r = static_cast<int>(cluster_ctarank()), stages = (a.Kb + kLinStageBlocks - 1) / kLinStageBlocks;
+    kb0 = stages * r / a.split * kLinStageBlocks;
+    kb1 = min(stages * (r + 1) / a.split * kLinStageBlocks, a.Kb);
+  }
 
   if (threadIdx.x == 0) {
     prefetch_tmap(&tmap_x);
@@ -455,8 +487,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), a.tmem_cols);
     }
   }
-  grid_dependency_wait();
-  grid_dependents_launch();  // only now: a kernel behind this one may rely on all that came before this one
+  if (!a.early) grid_dependency_wait();
   if (warp == 2) {
     // spans of each expert; an offset outside 0..M is clipped, one below an earlier one counts as that one
     int sum = 0, top = 0;
@@ -491,6 +522,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     __syncthreads();
   }
   tc_fence_after();
+  // Only now: a kernel behind this one may rely on all that came before this one, and must not take TMEM that a CTA
+  // of this grid still waits for.
+  if (!a.early) grid_dependents_launch();
   const uint32_t tmem_base = *tmem_slot;
   LinTiles tiles{first, start, count, a.E, a.tiles_n};
   const int total = tiles.total();
@@ -498,6 +532,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producer
     uint32_t s = 0, p = 0, armed = 0, par = 0;
+    bool waited = !a.early;
     for (int tile = first_tile; tile < total; tile += tile_step) {
       const LinTile t = tiles.at(tile);
       const int mine = t.n / kCtas;  // this CTA's rows of the codes
@@ -509,17 +544,35 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int nb = min(t.nb * kCtas + static_cast<int>(rank), a.nblk - 1);
       const int wrow = (t.e * a.nblk + nb) * a.Kb;
       const int row = t.row0 + static_cast<int>(rank) * mine;
-      for (int kb = 0; kb < a.Kb; kb += kLinStageBlocks) {
-        if (!mbar_wait(empty + 8 * s, p ^ 1, abort_flag, limit, kErrTimeoutProducer)) goto producer_done;
-        const uint32_t dst = base + s * a.stage_bytes, dst_x = dst + w_bytes;
-        const uint32_t bar = full + 8 * s;
+      // weights of the stage at ring position `at`
+      auto load_w = [&](int kb, uint32_t at) {
+        const uint32_t dst = base + at * a.stage_bytes, bar = full + 8 * at;
         if (leader) mbar_arrive_expect_tx(bar, bytes * kCtas);
-        if (check_bounds(bytes <= a.stage_bytes && wrow + kb < a.E * a.nblk * a.Kb && s < static_cast<uint32_t>(a.stages) &&
-                         t.row0 >= 0 && t.row0 < a.M)) {
-          // a last stage of one block loads what follows its weights, or the zeros behind the tensor: no MMA reads it
+        if (!check_bounds(bytes <= a.stage_bytes && wrow + kb < a.E * a.nblk * a.Kb && at < static_cast<uint32_t>(a.stages)))
+          return;
+        // a last stage of one block loads what follows its weights, or the zeros behind the tensor: no MMA reads it
+        if (kPair) {
+          tma_load_2d_pair(dst, &tmap_w, map_to_cta(bar, 0), 0, (wrow + kb) * kFp8Block);
+        } else {
+          tma_load_2d(dst, &tmap_w, bar, 0, (wrow + kb) * kFp8Block);
+        }
+      };
+      int ahead = kb0;  // weights loaded up to here
+      if (!waited) {    // the ring is empty: fill it with weights, then wait for the rows' codes
+        for (int i = 0; i < a.stages && ahead < kb1; ++i, ahead += kLinStageBlocks) load_w(ahead, s + i);
+        grid_dependency_wait();
+        waited = true;
+      }
+      for (int kb = kb0; kb < kb1; kb += kLinStageBlocks) {
+        const uint32_t dst_x = base + s * a.stage_bytes + w_bytes;
+        const uint32_t bar = full + 8 * s;
+        if (kb >= ahead) {
+          if (!mbar_wait(empty + 8 * s, p ^ 1, abort_flag, limit, kErrTimeoutProducer)) goto producer_done;
+          load_w(kb, s);
+        }
+        if (check_bounds(t.row0 >= 0 && t.row0 < a.M)) {
           if (kPair) {
             const uint32_t lead = map_to_cta(bar, 0);
-            tma_load_2d_pair(dst, &tmap_w, lead, 0, (wrow + kb) * kFp8Block);
             if (whole) {
               tma_load_3d<true>(dst_x, &tmap_x, lead, 0, row, kb);
             } else {
@@ -528,7 +581,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                                   &tmap_xs, lead, 0, row + i / kLinStageBlocks * kLinBoxRows, kb + i % kLinStageBlocks);
             }
           } else {
-            tma_load_2d(dst, &tmap_w, bar, 0, (wrow + kb) * kFp8Block);
             if (whole) {
               tma_load_3d<false>(dst_x, &tmap_x, bar, 0, row, kb);
             } else {
@@ -573,7 +625,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint64_t ad0 = sw128_kmajor_desc(base, 1024u);
     const uint64_t bd0 = sw128_kmajor_desc(base + kLinStageBlocks * kLinATile, 1024u);
     const uint32_t stage16 = a.stage_bytes >> 4, rows16 = static_cast<uint32_t>(a.box_rows) * 8u;
-    const int last_steps = (a.Kb - 1) % kLinStageBlocks * 4 + a.last_ksteps;  // 32-channel steps of a tile's last stage
+    // 32-channel steps of the tile's last stage
+    const int last_steps = kb1 < a.Kb ? 4 * kLinStageBlocks : (a.Kb - 1) % kLinStageBlocks * 4 + a.last_ksteps;
     uint32_t s = 0, p = 0, g = 0, gp = 0, c = 0, cp = 0;
     bool issued = false, ok = true, full_ready = false, sf_ready = false;
     for (int tile = first_tile; tile < total && ok; tile += tile_step) {
@@ -584,9 +637,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         break;
       }
       uint32_t acc = 0;  // the tile's first MMA overwrites the accumulator
-      for (int kb = 0; kb < a.Kb; kb += kLinStageBlocks) {
-        const bool last = kb + kLinStageBlocks >= a.Kb, first_half = (kb & 3) == 0, group_end = !first_half || last;
-        if (first_half && !sf_ready && !(ok = wait(sf_full + 8 * g, gp))) break;
+      for (int kb = kb0; kb < kb1; kb += kLinStageBlocks) {
+        const bool last = kb + kLinStageBlocks >= kb1, first_half = (kb & 3) == 0, group_end = !first_half || last;
+        if ((first_half || kb == kb0) && !sf_ready && !(ok = wait(sf_full + 8 * g, gp))) break;
         if (!full_ready && !(ok = wait(full + 8 * s, p))) break;
         tc_fence_after();
         const uint32_t ns = s + 1 == static_cast<uint32_t>(a.stages) ? 0u : s + 1, np = ns ? p : p ^ 1u;
@@ -649,6 +702,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // of column j.
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
     constexpr int kRowCols = kLinSfCols<kPair> - 4;
+    if (a.early) {
+      grid_dependency_wait();
+      grid_dependents_launch();
+    }
     uint32_t g = 0, gp = 0;
     bool ok = true;
     for (int tile = first_tile; tile < total && ok; tile += tile_step) {
@@ -665,13 +722,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               32 * j < t.n && row < a.M ? __ldcg(a.x_scale + static_cast<int64_t>(kg) * a.M + row) : 0x7F7F7F7Fu;
         }
       };
-      load(0);
-      for (int kg = 0; kg < a.kgroups; ++kg) {
+      const int kg0 = kb0 >> 2, kg1 = (kb1 + 3) >> 2;
+      load(kg0);
+      for (int kg = kg0; kg < kg1; ++kg) {
         uint32_t w[4 + kRowCols];
         w[0] = w[1] = w[2] = w[3] = next[0];
 #pragma unroll
         for (int j = 0; j < kRowCols; ++j) w[4 + j] = next[1 + j];
-        if (kg + 1 < a.kgroups) load(kg + 1);
+        if (kg + 1 < kg1) load(kg + 1);
         int got = 1;
         if (lane == 0) got = mbar_wait(sf_empty + 8 * g, gp ^ 1, abort_flag, limit, kErrTimeoutConvert);
         if (!(ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0)) break;
@@ -713,7 +771,30 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint32_t ld_line = static_cast<uint32_t>(lane >> 2), ld_grp = static_cast<uint32_t>(lane & 3);
     const uint32_t ld_addr = buf + ld_line * 64u + ((ld_grp ^ ((ld_line >> 1) & 3u)) << 4);
     uint32_t c = 0, cp = 0;
-    for (int tile = first_tile; tile < total; tile += tile_step) {
+    if (a.early) grid_dependency_wait();
+    if (split && first_tile < total) {
+      // this CTA's sums into its ring (every stage has been read): [row][128 channels] of fp32
+      const LinTile t = tiles.at(first_tile);
+      int got = 1;
+      if (lane == 0) got = mbar_wait(acc_full, 0, abort_flag, limit, kErrTimeoutEpilogue);
+      if (__shfl_sync(0xFFFFFFFFu, got, 0)) {
+        __syncwarp();
+        tc_fence_after();
+        for (int r0 = 0; r0 < t.rows; r0 += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(r0), v);
+          tmem_ld_wait(v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (r0 + j < t.rows)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + static_cast<uint32_t>((r0 + j) * kFp8Block + q * 32 + lane) * 4u),
+                           "r"(v[j])
+                           : "memory");
+        }
+        tc_fence_before();
+      }
+    }
+    for (int tile = split ? total : first_tile; tile < total; tile += tile_step) {
       const LinTile t = tiles.at(tile);
       const int ch0 = (t.nb * kCtas + static_cast<int>(rank)) * kFp8Block + q * 32;  // this warp's first channel
       float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // bias of channels ch0 + 8 i + lane / 4
@@ -757,16 +838,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                          : "r"(ld_addr + static_cast<uint32_t>(step) * 512u));
-            __nv_bfloat16* const dst = a.out + (t.row0 + r) * a.ldo + ch;
-            if (a.vec_out && ch + 8 <= a.N) {
-              *reinterpret_cast<uint4*>(dst) = w;
-            } else {
-              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (ch + i < a.N)
-                  reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(u[i >> 1] >> ((i & 1) * 16));
-            }
+            store_bf16x8(a.out + (t.row0 + r) * a.ldo + ch, w, a.N - ch, a.vec_out != 0);
           }
         }
       }
@@ -785,6 +857,41 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 
   __syncwarp();
+  if (split) {
+    cluster_sync();  // every CTA's sums are in its shared memory
+    if (first_tile < total) {
+      // each CTA adds and writes its share of the tile's groups of 8 channels
+      const LinTile t = tiles.at(first_tile);
+      const int r = static_cast<int>(cluster_ctarank()), items = t.rows * (kFp8Block / 8);
+      for (int i = items * r / a.split + static_cast<int>(threadIdx.x); i < items * (r + 1) / a.split; i += kLinThreads) {
+        const int row = i / (kFp8Block / 8), ch = t.nb * kFp8Block + i % (kFp8Block / 8) * 8;
+        if (ch >= a.N || !check_bounds(t.row0 + row < a.M)) continue;
+        float v[8] = {};
+        for (int k = 0; k < a.split; ++k) {
+          const uint32_t src = map_to_cta(base + static_cast<uint32_t>(i) * 32u, static_cast<uint32_t>(k));
+          float w[8];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(w[j]), "=f"(w[j + 1]), "=f"(w[j + 2]), "=f"(w[j + 3])
+                         : "r"(src + static_cast<uint32_t>(j) * 4u));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = k == 0 ? w[j] : v[j] + w[j];
+        }
+        const __nv_bfloat16* const be = a.bias ? a.bias + static_cast<int64_t>(t.e) * a.N + ch : nullptr;
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float b0 = be && ch + j < a.N ? __bfloat162float(be[j]) : 0.0f;
+          const float b1 = be && ch + j + 1 < a.N ? __bfloat162float(be[j + 1]) : 0.0f;
+          const __nv_bfloat162 p2 = __floats2bfloat162_rn(v[j] + b0, v[j + 1] + b1);
+          u[j >> 1] = *reinterpret_cast<const uint32_t*>(&p2);
+        }
+        store_bf16x8(a.out + (t.row0 + row) * a.ldo + ch, make_uint4(u[0], u[1], u[2], u[3]), a.N - ch, a.vec_out != 0);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another may still read its sums
+  }
   tc_fence_before();
   if (kPair) {
     cluster_sync();  // neither CTA leaves while its partner may still touch its memory

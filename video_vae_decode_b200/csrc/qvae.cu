@@ -583,7 +583,7 @@ int launch_quant_from_amax(const void* x, int64_t numel, const uint32_t* amax, i
 constexpr int64_t kLinMaxRows = int64_t{1} << 30;      // rows of x in a call
 constexpr int64_t kLinMaxChannels = int64_t{1} << 20;  // N, K
 
-std::atomic<int32_t> g_lin_force[3] = {};  // NT, mode (1 single CTA, 2 CTA pair), cap on the CTAs; 0 = automatic
+std::atomic<int32_t> g_lin_force[4] = {};  // NT, mode (1 single CTA, 2 CTA pair), split, cap on the CTAs; 0 = automatic
 bool g_lin_attr_set[kMaxDevices][2] = {};
 int g_lin_max_clusters[kMaxDevices] = {0};
 
@@ -591,6 +591,7 @@ int g_lin_max_clusters[kMaxDevices] = {0};
 struct LinPlan {
   bool pair;
   int NT;             // most rows of a tile
+  int split;          // CTAs that share a tile along K
   int64_t max_tiles;  // tiles of any offsets
 };
 
@@ -600,33 +601,40 @@ int64_t linear_tiles(int64_t E, int64_t M, int64_t nblk, bool grouped, bool pair
   return spans * (pair ? ceil_div(nblk, 2) : nblk);
 }
 
-// The tiling with the least estimated time.  A launch takes waves of tiles, one to an SM (to two SMs: a CTA pair); a
-// tile takes Kb * 4 MMAs and what its epilogue leaves exposed.
-LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms) {
+// The tiling with the least estimated time, in SM cycles.  A launch takes waves of tiles, one to an SM (to two SMs: a
+// CTA pair); a tile takes its MMAs or the loads of its weights, whichever is longer, and what its epilogue leaves exposed.
+LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms, bool forced = true) {
   const int64_t nblk = ceil_div(N, qvae::kFp8Block), Kb = ceil_div(K, qvae::kFp8Block);
+  const int64_t stages = ceil_div(Kb, qvae::kLinStageBlocks);
   const int64_t busy = grouped ? std::min(E, M) : 1;     // experts that have rows, at most
   const double rows = static_cast<double>(M) / busy;     // of one of them
   LinPlan best = {};
   double least = 0;
   for (int mode = 1; mode <= 2; ++mode) {
-    if (g_lin_force[1] && mode != g_lin_force[1]) continue;
+    if (forced && g_lin_force[1] && mode != g_lin_force[1]) continue;
     const bool pair = mode == 2;
     const int most = pair ? qvae::kLinMaxNT<true> : qvae::kLinMaxNT<false>;
     for (int nt = 16; nt <= most; nt += 16) {
-      if (g_lin_force[0] && nt != std::min<int>(g_lin_force[0], most)) continue;
+      if (forced && g_lin_force[0] && nt != std::min<int>(g_lin_force[0], most)) continue;
       const double spans = busy * std::ceil(rows / nt);
       const double tiles = spans * (pair ? ceil_div(nblk, 2) : nblk);
       const double n = std::min<double>(nt, std::ceil(rows / std::ceil(rows / nt) / 16) * 16);
-      const double mma = pair ? std::max(72.0, 0.56 * n) : std::max(64.0, 0.8 * n);
-      const double tile = Kb * 4 * mma + 600.0 + (pair ? 4.0 : 4.0) * n;
-      const double time = std::ceil(tiles / (pair ? sms / 2 : sms)) * tile;
-      if (!best.NT || time < least) {
-        best = {pair, nt, linear_tiles(E, M, nblk, grouped, pair, nt)};
-        least = time;
+      const double mma = pair ? std::max(72.0, 0.56 * n) : std::max(78.0, 0.9 * n);
+      for (int split = 1; split <= (pair ? 1 : 8); ++split) {
+        if (split > stages || (forced && g_lin_force[2] && split != std::min<int64_t>(pair ? 1 : g_lin_force[2].load(), stages))) continue;
+        // one tile to a cluster: what the offsets give at most must fit the device
+        if (split > 1 && linear_tiles(E, M, nblk, grouped, pair, nt) * split > 2 * sms) continue;
+        const double part = ceil_div(stages, split) * qvae::kLinStageBlocks * std::max(4 * mma, 420.0);
+        const double tile = part + 3000.0 + 4.0 * n + (split > 1 ? 1500.0 + 6.0 * n : 0.0);
+        const double time = std::ceil(tiles * split / (pair ? sms / 2 : sms)) * tile;
+        if (!best.NT || time < least) {
+          best = {pair, nt, split, linear_tiles(E, M, nblk, grouped, pair, nt)};
+          least = time;
+        }
       }
     }
   }
-  return best;
+  return best.NT ? best : plan_linear(E, M, N, K, grouped, sms, false);  // nothing that was forced fits
 }
 
 int check_linear(int64_t E, int64_t M, int64_t N, int64_t K) {
@@ -667,10 +675,11 @@ int launch_fp8_quant(int64_t M, int64_t K, int op, const void* x, int64_t ldx, u
   return QVAE_OK;
 }
 
-// offsets null: one span of M rows.
+// offsets null: one span of M rows.  early: the kernel before this one on the stream is the quantiser, which lets this
+// one start only when all that came before it has finished.
 int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq, const uint32_t* x_scale,
                   const int32_t* offsets, const uint8_t* wq, const uint8_t* w_scale, const void* bias, void* out,
-                  int64_t ldo, cudaStream_t stream) {
+                  int64_t ldo, cudaStream_t stream, bool early = false) {
   int rc = check_linear(E, M, N, K);
   if (rc) return rc;
   if (M == 0) return QVAE_OK;
@@ -694,20 +703,31 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.kgroups = (a.Kb + 3) / 4;
   const LinPlan plan = plan_linear(E, M, N, K, offsets != nullptr, sms);
   if (plan.max_tiles > INT32_MAX / 2) return QVAE_ERR_SHAPE;
-  const int ctas = plan.pair ? 2 : 1;
+  const int ctas = plan.pair ? 2 : plan.split;  // of a tile
   a.NT = plan.NT;
-  a.tiles_n = (a.nblk + ctas - 1) / ctas;
-  a.box_rows = (a.NT / ctas + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
+  a.split = plan.split;
+  a.early = early ? 1 : 0;
+  a.tiles_n = plan.pair ? (a.nblk + 1) / 2 : a.nblk;
+  a.box_rows = (a.NT / (plan.pair ? 2 : 1) + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
   a.stage_bytes = qvae::kLinStageBlocks * (qvae::kLinATile + static_cast<uint32_t>(a.box_rows) * 128u);
   const uint32_t rest = 1024u + qvae::kLinEpiWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u +
                         4u * static_cast<uint32_t>(3 * E + 1);
-  a.stages = std::min<int>(qvae::kLinMaxStages, (kSmemLimit - rest) / a.stage_bytes);
-  const uint32_t smem = rest + a.stages * a.stage_bytes;
-  // two accumulators (the epilogue reads 32 columns at a time) and two sets of scale words
+  // (clusters with one tile each may sit two to an SM)
+  const uint32_t room = plan.split > 1 && plan.max_tiles * plan.split > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
+  a.stages = std::min<int>(qvae::kLinMaxStages, (room - rest) / a.stage_bytes);
+  if (plan.split > 1) a.stages = std::min<int>(a.stages, ceil_div(ceil_div(a.Kb, qvae::kLinStageBlocks), plan.split));
+  // the ring also takes a split tile's sums
+  const uint32_t ring = std::max(a.stages * a.stage_bytes, plan.split > 1 ? a.NT * qvae::kFp8Block * 4u : 0u);
+  // Clusters wait for one another's CTAs, and a CTA for its TMEM: no two CTAs that can share an SM may want more than
+  // its 512 columns.  A split CTA takes at most 256 and a third of the shared memory, so that two fit and three do not,
+  // and none fits beside a CTA that takes more columns (those take 170 KB or more).
+  constexpr uint32_t kSplitSmem = 78 * 1024;
+  const uint32_t smem = std::max(rest + ring, plan.split > 1 ? kSplitSmem : 0u);
+  // two accumulators (a split CTA has one tile: one), read 32 columns at a time, and two sets of scale words
   const uint32_t sf_cols = plan.pair ? qvae::kLinSfCols<true> : qvae::kLinSfCols<false>;
   a.acc_cols = static_cast<uint32_t>(a.NT);
-  a.sf_col = 2 * a.acc_cols;
-  const uint32_t cols = std::max(a.sf_col + 2 * sf_cols, a.acc_cols + (a.acc_cols + 31) / 32 * 32);
+  a.sf_col = (plan.split > 1 ? 1 : 2) * a.acc_cols;
+  const uint32_t cols = std::max(a.sf_col + 2 * sf_cols, a.sf_col - a.acc_cols + (a.acc_cols + 31) / 32 * 32);
   a.tmem_cols = 32;
   while (a.tmem_cols < cols) a.tmem_cols <<= 1;
   a.vec_out = aligned16(out) && (ldo % 8 == 0 || M == 1);
@@ -746,8 +766,9 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     if ((rc = max_pairs(kernel, qvae::kLinThreads, sms, &g_lin_max_clusters[dev]))) return rc;
     grid = 2 * g_lin_max_clusters[dev];
   }
-  if (const int cap = g_lin_force[2]) grid = std::min(grid, cap);
+  if (const int cap = g_lin_force[3]) grid = std::min(grid, cap);
   grid = static_cast<int>(std::min<int64_t>(plan.max_tiles * ctas, std::max(grid / ctas, 1) * ctas));
+  if (plan.split > 1) grid = static_cast<int>(plan.max_tiles) * ctas;
   QVAE_CUDA(launch_dependent(kernel, dim3(grid), qvae::kLinThreads, smem, stream, ctas, tmap_x, tmap_xs, tmap_w,
                              a));
   return QVAE_OK;
@@ -770,7 +791,7 @@ int launch_linear_fused(int64_t E, int64_t M, int64_t N, int64_t K, int op, cons
   uint8_t* const xq = static_cast<uint8_t*>(workspace);
   uint32_t* const x_scale = reinterpret_cast<uint32_t*>(xq + round256(qvae_fp8_code_bytes(M, K)));
   if ((rc = launch_fp8_quant(M, K, op, x, ldx, xq, x_scale, stream))) return rc;
-  return launch_linear(E, M, N, K, xq, x_scale, offsets, wq, w_scale, bias, out, ldo, stream);
+  return launch_linear(E, M, N, K, xq, x_scale, offsets, wq, w_scale, bias, out, ldo, stream, true);
 }
 
 }  // namespace
@@ -1271,16 +1292,18 @@ int qvae_set_fused_quant(int32_t on) {
   return QVAE_OK;
 }
 
-int qvae_set_linear_tiling(int32_t NT, int32_t mode, int32_t max_ctas) {
-  if (NT < 0 || NT > qvae::kLinMaxNT<true> || NT % 16 || mode < 0 || mode > 2 || max_ctas < 0) return QVAE_ERR_ARG;
+int qvae_set_linear_tiling(int32_t NT, int32_t mode, int32_t split, int32_t max_ctas) {
+  if (NT < 0 || NT > qvae::kLinMaxNT<true> || NT % 16 || mode < 0 || mode > 2 || split < 0 || split > 8 || max_ctas < 0)
+    return QVAE_ERR_ARG;
   g_lin_force[0] = NT;
   g_lin_force[1] = mode;
-  g_lin_force[2] = max_ctas;
+  g_lin_force[2] = split;
+  g_lin_force[3] = max_ctas;
   return QVAE_OK;
 }
 
-int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* out2) {
-  if (!out2) return QVAE_ERR_ARG;
+int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* out3) {
+  if (!out3) return QVAE_ERR_ARG;
   const int rc = check_linear(std::max(E, 1), M, N, K);
   if (rc) return rc;
   if (E < 0) return QVAE_ERR_ARG;
@@ -1288,8 +1311,9 @@ int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* 
   if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) sm_count(dev, &sms);
   cudaGetLastError();
   const LinPlan plan = plan_linear(std::max(E, 1), std::max<int64_t>(M, 1), N, K, E > 0, sms);
-  out2[0] = plan.NT;
-  out2[1] = plan.pair ? 2 : 1;
+  out3[0] = plan.NT;
+  out3[1] = plan.pair ? 2 : 1;
+  out3[2] = plan.split;
   return QVAE_OK;
 }
 

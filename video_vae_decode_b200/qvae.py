@@ -120,7 +120,7 @@ def lib():
             "qvae_linear_fp8": ([i64, i32, i32, p, p, p, p, p, p, i64, p], ctypes.c_int),
             "qvae_linear_fp8_grouped": ([i32, i64, i32, i32, p, p, p, p, p, p, p, i64, p], ctypes.c_int),
             "qvae_linear_fp8_fused": ([i64, i32, i32, i32, p, i64, p, p, p, p, i64, p, sz, p], ctypes.c_int),
-            "qvae_set_linear_tiling": ([i32, i32, i32], ctypes.c_int),
+            "qvae_set_linear_tiling": ([i32, i32, i32, i32], ctypes.c_int),
             "qvae_get_linear_tiling": ([i32, i64, i32, i32, ctypes.POINTER(i32)], ctypes.c_int),
             "qvae_linear_fp8_grouped_fused": ([i32, i64, i32, i32, i32, p, i64, p, p, p, p, p, i64, p, sz, p],
                                               ctypes.c_int),
@@ -685,12 +685,12 @@ def qvae_get_conv_tiling(N, T, H, W, Cin, Cout, variant: int = 0) -> dict:
     return dict(zip(("MS", "NT", "SA", "SB", "acc_buffers", "ctas", "mode", "G"), list(out)))
 
 
-def qvae_set_linear_tiling(NT=0, mode=0, max_ctas=0) -> None:
-    _check("qvae_set_linear_tiling", lib().qvae_set_linear_tiling(NT, mode, max_ctas))
+def qvae_set_linear_tiling(NT=0, mode=0, split=0, max_ctas=0) -> None:
+    _check("qvae_set_linear_tiling", lib().qvae_set_linear_tiling(NT, mode, split, max_ctas))
 
 
 def qvae_get_linear_tiling(E, M, N, K) -> dict:
     """E = 0: a single layer; else grouped by E experts."""
-    out = (ctypes.c_int32 * 2)()
+    out = (ctypes.c_int32 * 3)()
     _check("qvae_get_linear_tiling", lib().qvae_get_linear_tiling(E, M, N, K, out))
-    return dict(zip(("NT", "mode"), list(out)))
+    return dict(zip(("NT", "mode", "split"), list(out)))
