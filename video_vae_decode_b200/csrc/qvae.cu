@@ -637,6 +637,33 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
   return best.NT ? best : plan_linear(E, M, N, K, grouped, sms, false);  // nothing that was forced fits
 }
 
+// plan_linear (about 1 us of host time) for sizes that the calling thread used lately is looked up.
+LinPlan known_plan(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms) {
+  struct Entry {
+    int64_t E = 0, M = 0, N = 0, K = 0;
+    int grouped = -1, sms = 0, force = 0;
+    LinPlan plan = {};
+  };
+  constexpr int kEntries = 16;
+  thread_local Entry known[kEntries];
+  thread_local int next = 0;
+  const int force = g_lin_force[0] | g_lin_force[1] << 8 | g_lin_force[2] << 16;
+  for (const Entry& k : known)
+    if (k.M == M && k.N == N && k.K == K && k.E == E && k.grouped == grouped && k.sms == sms && k.force == force)
+      return k.plan;
+  Entry& k = known[next];
+  next = (next + 1) % kEntries;
+  k.plan = plan_linear(E, M, N, K, grouped, sms);
+  k.E = E;
+  k.M = M;
+  k.N = N;
+  k.K = K;
+  k.grouped = grouped;
+  k.sms = sms;
+  k.force = force;
+  return k.plan;
+}
+
 int check_linear(int64_t E, int64_t M, int64_t N, int64_t K) {
   if (E < 0 || M < 0 || N < 0 || K < 0) return QVAE_ERR_ARG;
   if (E < 1 || E > qvae::kLinMaxExperts || N < 1 || N > kLinMaxChannels || K < 1 || K > kLinMaxChannels ||
@@ -701,7 +728,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.last_ksteps = static_cast<int>(ceil_div(K - int64_t{a.Kb - 1} * qvae::kFp8Block, 32));
   a.nblk = static_cast<int>(ceil_div(N, qvae::kFp8Block));
   a.kgroups = (a.Kb + 3) / 4;
-  const LinPlan plan = plan_linear(E, M, N, K, offsets != nullptr, sms);
+  const LinPlan plan = known_plan(E, M, N, K, offsets != nullptr, sms);
   if (plan.max_tiles > INT32_MAX / 2) return QVAE_ERR_SHAPE;
   const int ctas = plan.pair ? 2 : plan.split;  // of a tile
   a.NT = plan.NT;

@@ -474,59 +474,73 @@ def qvae_fp8_workspace_bytes(M: int, K: int) -> int:
     return int(lib().qvae_fp8_workspace_bytes(M, K))
 
 
-def _want(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
-def _buffer(t: torch.Tensor, dtype: torch.dtype, count: int, device: torch.device, name: str) -> int:
-    """Address of a contiguous tensor of at least `count` elements."""
-    _want(t.dtype == dtype and t.device == device and t.is_contiguous() and t.numel() >= count,
-          f"{name}: a contiguous {dtype} tensor of {count} elements on {device} is needed")
+def _buffer(t: torch.Tensor, dtype: torch.dtype, count: int, device: int, name: str) -> int:
+    """Address of a contiguous tensor of at least `count` elements on a device."""
+    if t.get_device() != device or t.dtype != dtype or not t.is_contiguous() or t.numel() < count:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of {count} elements on cuda:{device} is needed")
     return t.data_ptr()
 
 
-def _row_stride(t: torch.Tensor, columns: int, device: torch.device, name: str) -> int:
+def _row_stride(t: torch.Tensor, columns: int, device: int, name: str) -> int:
     """Elements between the rows of a bf16 matrix [M, columns] whose columns are adjacent."""
-    _want(t.dtype == torch.bfloat16 and t.device == device and t.dim() == 2 and t.shape[1] == columns,
-          f"{name}: a bf16 matrix of {columns} columns on {device} is needed")
-    ld = t.stride(0) if t.shape[0] > 1 else columns
-    _want((columns == 1 or t.stride(1) == 1) and ld >= columns,
-          f"{name}: rows of adjacent columns that do not overlap are needed")
+    if t.dtype != torch.bfloat16 or t.get_device() != device or t.dim() != 2 or t.size(1) != columns:
+        raise ValueError(f"{name}: a bf16 matrix of {columns} columns on cuda:{device} is needed")
+    ld = t.stride(0) if t.size(0) > 1 else columns
+    if ld < columns or (columns > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: rows of adjacent columns that do not overlap are needed")
     return ld
 
 
-def _on_stream(device: torch.device, stream):
-    """Context for a call on `device` and `stream` (None: the device's current stream), and that stream's handle."""
+def _device(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is needed")
+    return t.get_device()
+
+
+@contextlib.contextmanager
+def _elsewhere(device: int, stream):
+    """A device that is not the current one, or a stream that is not its current one: the call's handle."""
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
-        if device.index == torch.cuda.current_device():
-            return contextlib.nullcontext(), handle
-        return torch.cuda.device(device), handle
+        with torch.cuda.device(device):
+            yield torch.cuda.current_stream().cuda_stream
+        return
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
-    _want(stream.device == device, f"the stream is on {stream.device}, the tensors are on {device}")
-    return torch.cuda.stream(stream), stream.cuda_stream
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                           torch.device("cuda", device))
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{device}")
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
 
 
-def _cuda(t: torch.Tensor, name: str) -> torch.device:
-    _want(isinstance(t, torch.Tensor) and t.is_cuda, f"{name}: a CUDA tensor is needed")
-    return t.device
+# The current stream's handle without a Stream object around it (1.3 us less a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _run(device: int, stream, call, *args):
+    """call(handle, *args) on `device` and `stream` (None: the device's current stream)."""
+    if stream is None and device == torch.cuda.current_device():
+        return call(_raw_stream(device), *args)
+    with _elsewhere(device, stream) as handle:
+        return call(handle, *args)
 
 
 def fp8_quantize_weights(w: torch.Tensor, stream=None) -> Fp8Weights:
     """Quantise and pack bf16 weights [N, K] or, one matrix to an expert, [E, N, K]."""
-    device = _cuda(w, "w")
-    _want(w.dtype == torch.bfloat16 and w.dim() in (2, 3) and w.is_contiguous(),
-          "w: contiguous bf16 weights [N, K] or [E, N, K] are needed")
+    device = _device(w, "w")
+    if w.dtype != torch.bfloat16 or w.dim() not in (2, 3) or not w.is_contiguous():
+        raise ValueError("w: contiguous bf16 weights [N, K] or [E, N, K] are needed")
     E, N, K = (1, *w.shape) if w.dim() == 2 else w.shape
-    ctx, handle = _on_stream(device, stream)
-    with ctx:
-        wq = torch.empty(qvae_fp8_packed_weight_bytes(E, N, K), dtype=torch.uint8, device=device)
-        ws = torch.empty(qvae_fp8_weight_scale_bytes(E, N, K), dtype=torch.uint8, device=device)
+
+    def call(handle):
+        wq = torch.empty(qvae_fp8_packed_weight_bytes(E, N, K), dtype=torch.uint8, device=w.device)
+        ws = torch.empty(qvae_fp8_weight_scale_bytes(E, N, K), dtype=torch.uint8, device=w.device)
         _check("qvae_fp8_quantize_weights",
                lib().qvae_fp8_quantize_weights(E, N, K, w.data_ptr(), wq.data_ptr(), ws.data_ptr(), handle))
-    return Fp8Weights(wq, ws, E, N, K)
+        return Fp8Weights(wq, ws, E, N, K)
+
+    return _run(device, stream, call)
 
 
 def fp8_workspace(M: int, K: int, device="cuda") -> torch.Tensor:
@@ -537,63 +551,69 @@ def fp8_workspace(M: int, K: int, device="cuda") -> torch.Tensor:
 def fp8_quant_act(x: torch.Tensor, silu_mul: bool = False, stream=None):
     """Codes (uint8 [ceil(K/128), M, 128]) and scale words (int32 [ceil(K/512), M]) of bf16 rows x [M, K]
     (silu_mul: [M, 2 K], of which silu(x[:, :K]) * x[:, K:] is quantised)."""
-    device = _cuda(x, "x")
-    _want(x.dim() == 2 and x.shape[1] >= 1 and not (silu_mul and x.shape[1] % 2),
-          "x: a matrix is needed, with an even number of columns for silu_mul")
+    device = _device(x, "x")
+    if x.dim() != 2 or x.shape[1] < 1 or (silu_mul and x.shape[1] % 2):
+        raise ValueError("x: a matrix is needed, with an even number of columns for silu_mul")
     M, columns = x.shape
     K = columns // 2 if silu_mul else columns
     ld = _row_stride(x, columns, device, "x")
-    ctx, handle = _on_stream(device, stream)
-    with ctx:
-        xq = torch.empty((-(-K // 128), M, 128), dtype=torch.uint8, device=device)
-        xs = torch.empty((-(-K // 512), M), dtype=torch.int32, device=device)
+
+    def call(handle):
+        xq = torch.empty((-(-K // 128), M, 128), dtype=torch.uint8, device=x.device)
+        xs = torch.empty((-(-K // 512), M), dtype=torch.int32, device=x.device)
         _check("qvae_fp8_quant_act",
                lib().qvae_fp8_quant_act(M, K, QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN, x.data_ptr(), ld,
                                         xq.data_ptr(), xs.data_ptr(), handle))
-    return xq, xs
+        return xq, xs
+
+    return _run(device, stream, call)
 
 
-def _layer(device, weights, M, bias, out, offsets):
+def _layer(device: int, weights: Fp8Weights, M: int, bias, out, offsets):
     """Checks what every product takes; (row stride of out, addresses of weights, scales, bias, offsets)."""
-    E, N, K = weights.E, weights.N, weights.K
+    wq, w_scale, E, N, K = weights
     if offsets is None:
-        _want(E == 1, f"the weights hold {E} experts: use the grouped product")
+        if E != 1:
+            raise ValueError(f"the weights hold {E} experts: use the grouped product")
         po = None
     else:
         po = _buffer(offsets, torch.int32, E + 1, device, "offsets")
     pb = None
     if bias is not None:
-        _want(tuple(bias.shape) in ((E, N), (N,) if E == 1 else (E, N)), f"bias: [N] or [E, N] is needed, N = {N}, E = {E}")
+        if tuple(bias.shape) != (E, N) and (E != 1 or tuple(bias.shape) != (N,)):
+            raise ValueError(f"bias: [N] or [E, N] is needed, N = {N}, E = {E}")
         pb = _buffer(bias, torch.bfloat16, E * N, device, "bias")
     ldo = N
     if out is not None:
         ldo = _row_stride(out, N, device, "out")
-        _want(out.shape[0] == M, f"out: {M} rows are needed")
+        if out.size(0) != M:
+            raise ValueError(f"out: {M} rows are needed")
     blocks = E * -(-N // 128)
-    return (ldo, _buffer(weights.wq, torch.uint8, blocks * -(-K // 128) * 16384, device, "weights.wq"),
-            _buffer(weights.w_scale, torch.uint8, blocks * -(-K // 512) * 4, device, "weights.w_scale"), pb, po)
+    return (ldo, _buffer(wq, torch.uint8, blocks * -(-K // 128) * 16384, device, "weights.wq"),
+            _buffer(w_scale, torch.uint8, blocks * -(-K // 512) * 4, device, "weights.w_scale"), pb, po)
 
 
 def _product(name, xq, x_scale, weights, bias, out, offsets, stream):
-    device = _cuda(xq, "xq")
+    device = _device(xq, "xq")
     K = weights.K
-    _want(xq.dim() == 3 and xq.shape[0] == -(-K // 128) and xq.shape[2] == 128,
-          f"xq: codes [{-(-K // 128)}, rows, 128] of {K} input channels are needed")
+    if xq.dim() != 3 or xq.shape[0] != -(-K // 128) or xq.shape[2] != 128:
+        raise ValueError(f"xq: codes [{-(-K // 128)}, rows, 128] of {K} input channels are needed")
     M = xq.shape[1]
     px = _buffer(xq, torch.uint8, xq.numel(), device, "xq")
     ps = _buffer(x_scale, torch.int32, M * -(-K // 512), device, "x_scale")
     ldo, pw, pws, pb, po = _layer(device, weights, M, bias, out, offsets)
-    ctx, handle = _on_stream(device, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty((M, weights.N), dtype=torch.bfloat16, device=device)
-        if offsets is None:
-            status = lib().qvae_linear_fp8(M, weights.N, K, px, ps, pw, pws, pb, out.data_ptr(), ldo, handle)
+
+    def call(handle):
+        o = torch.empty((M, weights.N), dtype=torch.bfloat16, device=xq.device) if out is None else out
+        if po is None:
+            status = lib().qvae_linear_fp8(M, weights.N, K, px, ps, pw, pws, pb, o.data_ptr(), ldo, handle)
         else:
-            status = lib().qvae_linear_fp8_grouped(weights.E, M, weights.N, K, px, ps, po, pw, pws, pb,
-                                                   out.data_ptr(), ldo, handle)
-    _check(name, status)
-    return out
+            status = lib().qvae_linear_fp8_grouped(weights.E, M, weights.N, K, px, ps, po, pw, pws, pb, o.data_ptr(),
+                                                   ldo, handle)
+        _check(name, status)
+        return o
+
+    return _run(device, stream, call)
 
 
 def linear_fp8(xq: torch.Tensor, x_scale: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None,
@@ -607,32 +627,35 @@ def linear_fp8_grouped(xq: torch.Tensor, x_scale: torch.Tensor, offsets: torch.T
                        stream=None) -> torch.Tensor:
     """bf16 [M, N] of quantised rows sorted by expert: rows offsets[e]..offsets[e+1]-1 (int32, on the device) meet
     expert e's matrix; other rows of out are left as they are."""
-    _want(offsets is not None, "offsets: an int32 tensor is needed")
+    if offsets is None:
+        raise ValueError("offsets: an int32 tensor is needed")
     return _product("qvae_linear_fp8_grouped", xq, x_scale, weights, bias, out, offsets, stream)
 
 
-def _fused(name, x, weights, bias, silu_mul, out, workspace, offsets, stream):
-    device = _cuda(x, "x")
-    K = weights.K
-    ldx = _row_stride(x, 2 * K if silu_mul else K, device, "x")
-    M = x.shape[0]
-    ldo, pw, pws, pb, po = _layer(device, weights, M, bias, out, offsets)
+def _fused_call(handle, name, x, ldx, weights, silu_mul, out, ldo, workspace, device, pw, pws, pb, po):
+    M, N, K = x.size(0), weights.N, weights.K
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    if workspace is None:
+        workspace = fp8_workspace(M, K, x.device)
+    pk = _buffer(workspace, torch.uint8, 0, device, "workspace")
     op = QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN
-    ctx, handle = _on_stream(device, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty((M, weights.N), dtype=torch.bfloat16, device=device)
-        if workspace is None:
-            workspace = fp8_workspace(M, K, device)
-        pk = _buffer(workspace, torch.uint8, 0, device, "workspace")
-        if offsets is None:
-            status = lib().qvae_linear_fp8_fused(M, weights.N, K, op, x.data_ptr(), ldx, pw, pws, pb, out.data_ptr(),
-                                                 ldo, pk, workspace.numel(), handle)
-        else:
-            status = lib().qvae_linear_fp8_grouped_fused(weights.E, M, weights.N, K, op, x.data_ptr(), ldx, po, pw, pws,
-                                                         pb, out.data_ptr(), ldo, pk, workspace.numel(), handle)
-    _check(name, status)
+    if po is None:
+        status = lib().qvae_linear_fp8_fused(M, N, K, op, x.data_ptr(), ldx, pw, pws, pb, out.data_ptr(), ldo, pk,
+                                             workspace.numel(), handle)
+    else:
+        status = lib().qvae_linear_fp8_grouped_fused(weights.E, M, N, K, op, x.data_ptr(), ldx, po, pw, pws, pb,
+                                                     out.data_ptr(), ldo, pk, workspace.numel(), handle)
+    if status:
+        _check(name, status)
     return out
+
+
+def _fused(name, x, weights, bias, silu_mul, out, workspace, offsets, stream):
+    device = _device(x, "x")
+    ldx = _row_stride(x, 2 * weights.K if silu_mul else weights.K, device, "x")
+    ldo, pw, pws, pb, po = _layer(device, weights, x.size(0), bias, out, offsets)
+    return _run(device, stream, _fused_call, name, x, ldx, weights, silu_mul, out, ldo, workspace, device, pw, pws, pb, po)
 
 
 def linear_fp8_fused(x: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None, silu_mul: bool = False,
@@ -647,7 +670,8 @@ def linear_fp8_grouped_fused(x: torch.Tensor, offsets: torch.Tensor, weights: Fp
                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                              stream=None) -> torch.Tensor:
     """linear_fp8_grouped of bf16 rows, quantised on the way."""
-    _want(offsets is not None, "offsets: an int32 tensor is needed")
+    if offsets is None:
+        raise ValueError("offsets: an int32 tensor is needed")
     return _fused("qvae_linear_fp8_grouped_fused", x, weights, bias, silu_mul, out, workspace, offsets, stream)
 
 
