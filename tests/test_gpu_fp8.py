@@ -546,3 +546,37 @@ def test_tiles_split_along_k(q, nt, split):
                 check_product(out[o[i]:o[i + 1]], y, s, 2100)
     finally:
         q.qvae_set_linear_tiling()
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("split", [0, 1, 4])
+@pytest.mark.parametrize("m,n,k,extra", [(1, 128, 128, 0), (1, 300, 2048, 0), (3, 200, 8, 8), (7, 136, 1176, 16),
+                                         (16, 384, 1000, 0), (16, 128, 4096, 0), (5, 257, 264, 0)])
+def test_few_rows_quantised_by_the_product(q, m, n, k, extra, split, silu):
+    # one launch: the same codes and scales as the quantiser, so the sums differ by their order at most
+    x, w, b = rows(m, (2 if silu else 1) * k, m + n, extra), matrix((n, k), k), matrix((1, n), 3)[0]
+    if m > 4:
+        x[1] = 0.0
+        x[2, k - 1] = float("nan")
+    p = q.fp8_quantize_weights(w)
+    two = q.linear_fp8(*q.fp8_quant_act(x, silu_mul=silu), p, b)
+    try:
+        q.qvae_set_linear_tiling(16, 1, split)
+        one = q.linear_fp8_fused(x, p, b, silu_mul=silu)
+        same = q.linear_fp8(*q.fp8_quant_act(x, silu_mul=silu), p, b)   # the same tiling, quantised before
+        assert torch.equal(one.view(torch.int16), same.view(torch.int16))
+        many = rows(60, (2 if silu else 1) * k, 1, extra)               # several spans of 16 rows
+        assert torch.equal(q.linear_fp8_fused(many, p, b, silu_mul=silu),
+                           q.linear_fp8(*q.fp8_quant_act(many, silu_mul=silu), p, b))
+        o = torch.tensor([0, 20, 20, 21, 60], dtype=torch.int32, device="cuda")
+        pe = q.fp8_quantize_weights(matrix((4, n, k), 8))
+        assert torch.equal(q.linear_fp8_grouped_fused(many, o, pe, silu_mul=silu),
+                           q.linear_fp8_grouped(*q.fp8_quant_act(many, silu_mul=silu), o, pe))
+    finally:
+        q.qvae_set_linear_tiling()
+    assert q.qvae_get_error() == 0
+    assert torch.equal(torch.isnan(one), torch.isnan(two))
+    if not silu:
+        fine = [i for i in range(m) if not (m > 4 and i == 2)]
+        y, s = ref.linear(ref.act_values(x[fine]), ref.weight_values(w), b)
+        check_product(one[fine], y, s, k)

@@ -330,6 +330,11 @@ struct LinArgs {
   uint32_t stage_bytes;  // per 128-channel block of a stage: 16 KB of weights + box_rows rows of codes
   uint32_t acc_cols, sf_col, tmem_cols;
   int split;             // CTAs of a cluster that share a tile along K (1, or one tile to a cluster; single CTAs)
+  const __nv_bfloat16* x;  // (quantising variant) the rows, ldx apart
+  int64_t ldx;
+  int vec_x;             // (quantising variant) rows of x (and their second halves) start on 16 bytes
+  int silu;              // (quantising variant) rows are [gate | up]
+  uint32_t codes_bytes;  // (quantising variant) codes of a CTA's part of K
   int early;             // weights and offsets are final before the kernel before this one ends
   int vec_out;           // rows of out start on 16 bytes
   const int32_t* offsets;    // [E + 1] row offsets of the experts, or null (one span of M rows)
@@ -345,11 +350,15 @@ constexpr int kLinScaleWarps = 4, kLinEpiWarps = 4;
 constexpr int kLinThreads = 32 * (2 + kLinScaleWarps + kLinEpiWarps);
 constexpr int kLinMaxStages = 12;
 constexpr int kLinMaxExperts = 1024;
+constexpr int kLinMaxSplit = 8;                        // CTAs of a cluster that share a tile
 constexpr int kLinStageBlocks = 2;                     // 128-channel blocks of a pipeline stage
 constexpr int kLinBoxRows = 32;                        // rows of a small TMA box of codes
 constexpr int kLinSpanGroup = 16;                      // row spans walked under each output tile (see LinTiles)
 constexpr uint32_t kLinATile = kFp8Block * kFp8Block;  // bytes of one weight tile
 constexpr uint32_t kLinBars = 8 * (2 * kLinMaxStages + 4 + 4 + 1);
+// The variant that quantises its rows itself: rows of its tile and 128-channel blocks of its part of K, at most.
+constexpr int kLinFuseRows = 16, kLinFuseBlocks = 32;
+constexpr uint32_t kLinFuseScales = (kLinFuseBlocks / 4 + 1) * kLinFuseRows * 4;  // its scale words (a part may start inside a group)
 constexpr uint32_t kLinEpiBuf = 2048;                  // an epilogue warp's 32 rows x 32 channels of bf16
 // Most rows of a tile: two accumulators and two sets of scale words (4 columns of weights', 1 per 32 rows) fit the 512
 // columns of TMEM.
@@ -362,6 +371,22 @@ struct LinTile {
   int e, nb, row0, rows;
   int n;  // rows of the product: `rows` rounded up to the 16 that an MMA takes
 };
+
+// Tile `local` of an expert's `count` rows from `start` in `spans` spans.
+__device__ __forceinline__ LinTile lin_tile(int local, int spans, int tiles_n, int e, int start, int count) {
+  const int full = kLinSpanGroup * tiles_n;
+  const int g0 = local / full * kLinSpanGroup, in = local % full;
+  const int gs = min(kLinSpanGroup, spans - g0);
+  LinTile t;
+  t.e = e;
+  t.nb = in / gs;
+  const int per = ((count + spans - 1) / spans + 15) & ~15;
+  const int s = g0 + in % gs;
+  t.row0 = start + s * per;
+  t.rows = min(per, count - s * per);
+  t.n = (t.rows + 15) & ~15;
+  return t;
+}
 
 // The tiles of a launch: for each expert, its rows in spans of at most NT (as
 // even as multiples of 16 allow), and for each span every output tile.
@@ -377,20 +402,7 @@ struct LinTiles {
   __device__ __forceinline__ int total() const { return first[E] * tiles_n; }
   __device__ __forceinline__ LinTile at(int tile) {
     while (tile >= first[e + 1] * tiles_n) ++e;
-    const int spans = first[e + 1] - first[e];
-    const int local = tile - first[e] * tiles_n;
-    const int full = kLinSpanGroup * tiles_n;
-    const int g0 = local / full * kLinSpanGroup, in = local % full;
-    const int gs = min(kLinSpanGroup, spans - g0);
-    LinTile t;
-    t.e = e;
-    t.nb = in / gs;
-    const int per = ((count[e] + spans - 1) / spans + 15) & ~15;
-    const int s = g0 + in % gs;
-    t.row0 = start[e] + s * per;
-    t.rows = min(per, count[e] - s * per);
-    t.n = (t.rows + 15) & ~15;
-    return t;
+    return lin_tile(tile - first[e] * tiles_n, first[e + 1] - first[e], tiles_n, e, start[e], count[e]);
   }
 };
 
@@ -422,18 +434,28 @@ struct LinTiles {
 // of the ranks over distributed shared memory (no atomics: the same bits every
 // time, and no workspace), and written.
 //
+// kFuse (single CTAs, one tile each): the rows are bf16 and eight warps quantise
+// the CTA's part of them -- the codes, scales and outputs of the quantiser and
+// the product, in one launch.  Every CTA of a row does it again, so it is for
+// few rows (at most 16 to a tile).  It is done once, in front of the MMAs, while
+// the ring fills with weights, whose loads bound such calls: a stage at a time
+// beside the MMAs it measured slower than the two launches (its chain of
+// barriers took 2200 cycles a stage).
+//
 // Launched as a programmatic dependent.  With `early` (the quantiser of the
 // same call in front) the first weights are loaded before its end is waited
 // for; codes, scales and everything written wait for it.
-template <bool kPair>
-__global__ void __launch_bounds__(kLinThreads, 1)
+template <bool kPair, bool kFuse>
+__global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_xs,
                       const __grid_constant__ CUtensorMap tmap_w, const LinArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  const uint32_t epi_stage = base + static_cast<uint32_t>(a.stages) * a.stage_bytes;
+  const uint32_t codes = base + static_cast<uint32_t>(a.stages) * a.stage_bytes;  // (kFuse) codes, then scale words
+  const uint32_t scale_words = codes + a.codes_bytes;
+  const uint32_t epi_stage = codes + (kFuse ? a.codes_bytes + kLinFuseScales : 0u);
   const uint32_t bars = epi_stage + kLinEpiWarps * kLinEpiBuf;
   const uint32_t full = bars, empty = full + 8 * kLinMaxStages;
   const uint32_t sf_full = empty + 8 * kLinMaxStages, sf_empty = sf_full + 16;
@@ -480,6 +502,36 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  // Weights of the stage at ring position `at`.  A last stage of one block loads what follows its weights, or the zeros
+  // behind the tensor: no MMA reads it.
+  auto load_w = [&](uint32_t at, int wrow, uint32_t bytes) {
+    const uint32_t dst = base + at * a.stage_bytes, bar = full + 8 * at;
+    if (leader) mbar_arrive_expect_tx(bar, bytes * kCtas);
+    if (!check_bounds(bytes <= a.stage_bytes && wrow >= 0 && wrow < a.E * a.nblk * a.Kb && at < static_cast<uint32_t>(a.stages)))
+      return;
+    if (kPair) {
+      tma_load_2d_pair(dst, &tmap_w, map_to_cta(bar, 0), 0, wrow * kFp8Block);
+    } else {
+      tma_load_2d(dst, &tmap_w, bar, 0, wrow * kFp8Block);
+    }
+  };
+  // Bytes of a stage of tile t: the weights and the boxes of codes.
+  auto stage_boxes = [&](const LinTile& t) { return (t.n / kCtas + kLinBoxRows - 1) / kLinBoxRows; };
+  auto stage_bytes = [&](const LinTile& t) {
+    return kLinStageBlocks * (kLinATile + (kFuse ? 0u : static_cast<uint32_t>(stage_boxes(t)) * (kLinBoxRows * 128u)));
+  };
+  // A single layer's first tile is known: its weights are asked for before anything else is set up.
+  int ahead = kb0;  // (thread 0) blocks of the first tile whose weights have been asked for
+  if (!kPair && threadIdx.x == 0 && !a.offsets) {
+    if (!a.early) grid_dependency_wait();
+    const int spans = (a.M + a.NT - 1) / a.NT;
+    if (first_tile < spans * a.tiles_n) {
+      const LinTile t = lin_tile(first_tile, spans, a.tiles_n, 0, 0, a.M);
+      for (uint32_t i = 0; i < static_cast<uint32_t>(a.stages) && ahead < kb1; ++i, ahead += kLinStageBlocks)
+        load_w(i, t.nb * a.Kb + ahead, stage_bytes(t));
+    }
+  }
+  __syncwarp();
   if (warp == 1) {
     if (kPair) {
       tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), a.tmem_cols);
@@ -529,6 +581,93 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   LinTiles tiles{first, start, count, a.E, a.tiles_n};
   const int total = tiles.total();
 
+  if (kFuse && warp >= 2 && first_tile < total) {
+    // ----------------------------------------------------------- quantisers
+    // The tile's rows, this CTA's part of K: 16 channels to a lane and eight
+    // lanes to a block, as in the quantiser; codes [block][16 rows][128] in the
+    // MMA's swizzled order and scale bytes in shared memory.  Then four of the
+    // warps put the scale words into TMEM: row l's at lane l.
+    const LinTile t = tiles.at(first_tile);
+    const int qw = warp - 2, sub = lane >> 3, col = lane & 7;
+    const int blocks = kb1 - kb0, items = t.rows * blocks;
+    constexpr int kWarps = kLinScaleWarps + kLinEpiWarps, kUnroll = 2;
+    for (int i0 = qw * 4; i0 < items; i0 += kUnroll * kWarps * 4) {
+      uint4 w[kUnroll][2], u[kUnroll][2];
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        const int item = i0 + r * kWarps * 4 + sub;
+        const int row = item / blocks, b = item - row * blocks;
+        const int64_t k = static_cast<int64_t>(kb0 + b) * kFp8Block + col * 16;
+        const uint16_t* const src = reinterpret_cast<const uint16_t*>(a.x) + (t.row0 + row) * a.ldx;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool in = item < items && k + 8 * h < a.K && check_bounds(t.row0 + row < a.M);
+          w[r][h] = u[r][h] = make_uint4(0u, 0u, 0u, 0u);
+          if (in) {
+            w[r][h] = a.vec_x ? load_bf16x8<true>(src, k + 8 * h, a.K) : load_bf16x8<false>(src, k + 8 * h, a.K);
+            if (a.silu)
+              u[r][h] = a.vec_x ? load_bf16x8<true>(src + a.K, k + 8 * h, a.K) : load_bf16x8<false>(src + a.K, k + 8 * h, a.K);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        const int item = i0 + r * kWarps * 4 + sub;
+        const int row = item / blocks, b = item - row * blocks;
+        float v[2][8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          widen_bf16x8(w[r][h], v[h]);
+          if (a.silu) {  // (zeros beyond K stay zeros)
+            float up[8];
+            widen_bf16x8(u[r][h], up);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[h][j] = silu_mul(v[h][j], up[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[h][j]));
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if (item >= items) continue;
+        const uint32_t byte = e8m0_of_amax(m);
+        const float inv = e8m0_reciprocal(byte);
+        const uint2 lo = e4m3x8(v[0], inv), hi = e4m3x8(v[1], inv);
+        const uint32_t line = static_cast<uint32_t>(b * kLinFuseRows + row);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(codes + line * 128u + static_cast<uint32_t>((col ^ (row & 7)) << 4)),
+                     "r"(lo.x), "r"(lo.y), "r"(hi.x), "r"(hi.y)
+                     : "memory");
+        // byte (kb & 3) of word [group][row]
+        const int kb = kb0 + b;
+        if (col == 0)
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(scale_words + static_cast<uint32_t>((((kb >> 2) - (kb0 >> 2)) * kLinFuseRows + row) * 4 + (kb & 3))),
+                       "r"(byte)
+                       : "memory");
+      }
+    }
+    fence_proxy_async_smem();  // the codes are read by the tensor cores
+    named_barrier_sync(1, 32 * kWarps);
+    if (warp < 2 + kLinScaleWarps) {
+      const uint32_t dst = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + a.sf_col;
+      const uint32_t* const ws = a.w_scale + static_cast<int64_t>(t.e * a.nblk + t.nb) * a.kgroups;
+      for (int kg = kb0 >> 2; kg < (kb1 + 3) >> 2; ++kg) {
+        const uint32_t g = static_cast<uint32_t>(kg - (kb0 >> 2));
+        uint32_t w[8] = {};
+        w[0] = w[1] = w[2] = w[3] = __ldcg(ws + kg);
+        asm volatile("ld.shared.u32 %0, [%1];"
+                     : "=r"(w[4])
+                     : "r"(scale_words + (g * kLinFuseRows + static_cast<uint32_t>(lane & (kLinFuseRows - 1))) * 4u));
+        tmem_st_x4(dst + g * kLinSfCols<kPair>, w);
+        tmem_st_x4(dst + g * kLinSfCols<kPair> + 4, w + 4);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sf_full);
+    }
+  }
+
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producer
     uint32_t s = 0, p = 0, armed = 0, par = 0;
@@ -536,42 +675,31 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     for (int tile = first_tile; tile < total; tile += tile_step) {
       const LinTile t = tiles.at(tile);
       const int mine = t.n / kCtas;  // this CTA's rows of the codes
-      const int boxes = (mine + kLinBoxRows - 1) / kLinBoxRows;
+      const int boxes = stage_boxes(t);
       const bool whole = boxes * kLinBoxRows == a.box_rows;
-      const uint32_t w_bytes = kLinStageBlocks * kLinATile, x_bytes = static_cast<uint32_t>(boxes) * (kLinBoxRows * 128u);
-      const uint32_t bytes = w_bytes + kLinStageBlocks * x_bytes;
+      const uint32_t bytes = stage_bytes(t);
       // the second CTA of the last pair may have no output block of its own: it reads the last one again
       const int nb = min(t.nb * kCtas + static_cast<int>(rank), a.nblk - 1);
       const int wrow = (t.e * a.nblk + nb) * a.Kb;
       const int row = t.row0 + static_cast<int>(rank) * mine;
-      // weights of the stage at ring position `at`
-      auto load_w = [&](int kb, uint32_t at) {
-        const uint32_t dst = base + at * a.stage_bytes, bar = full + 8 * at;
-        if (leader) mbar_arrive_expect_tx(bar, bytes * kCtas);
-        if (!check_bounds(bytes <= a.stage_bytes && wrow + kb < a.E * a.nblk * a.Kb && at < static_cast<uint32_t>(a.stages)))
-          return;
-        // a last stage of one block loads what follows its weights, or the zeros behind the tensor: no MMA reads it
-        if (kPair) {
-          tma_load_2d_pair(dst, &tmap_w, map_to_cta(bar, 0), 0, (wrow + kb) * kFp8Block);
-        } else {
-          tma_load_2d(dst, &tmap_w, bar, 0, (wrow + kb) * kFp8Block);
-        }
-      };
-      int ahead = kb0;  // weights loaded up to here
-      if (!waited) {    // the ring is empty: fill it with weights, then wait for the rows' codes
-        for (int i = 0; i < a.stages && ahead < kb1; ++i, ahead += kLinStageBlocks) load_w(ahead, s + i);
+      if (!waited) {  // the ring is empty: fill it with weights, then wait for the rows' codes
+        for (uint32_t i = (ahead - kb0) / kLinStageBlocks; i < static_cast<uint32_t>(a.stages) && ahead < kb1;
+             ++i, ahead += kLinStageBlocks)
+          load_w(i, wrow + ahead, bytes);
         grid_dependency_wait();
         waited = true;
       }
+      if (tile != first_tile) ahead = kb0;
       for (int kb = kb0; kb < kb1; kb += kLinStageBlocks) {
-        const uint32_t dst_x = base + s * a.stage_bytes + w_bytes;
+        const uint32_t dst_x = base + s * a.stage_bytes + kLinStageBlocks * kLinATile;
         const uint32_t bar = full + 8 * s;
         if (kb >= ahead) {
           if (!mbar_wait(empty + 8 * s, p ^ 1, abort_flag, limit, kErrTimeoutProducer)) goto producer_done;
-          load_w(kb, s);
+          load_w(s, wrow + kb, bytes);
         }
         if (check_bounds(t.row0 >= 0 && t.row0 < a.M)) {
-          if (kPair) {
+          if (kFuse) {  // no codes to load
+          } else if (kPair) {
             const uint32_t lead = map_to_cta(bar, 0);
             if (whole) {
               tma_load_3d<true>(dst_x, &tmap_x, lead, 0, row, kb);
@@ -623,8 +751,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     };
     const uint64_t ad0 = sw128_kmajor_desc(base, 1024u);
-    const uint64_t bd0 = sw128_kmajor_desc(base + kLinStageBlocks * kLinATile, 1024u);
-    const uint32_t stage16 = a.stage_bytes >> 4, rows16 = static_cast<uint32_t>(a.box_rows) * 8u;
+    const uint64_t bd0 = sw128_kmajor_desc(kFuse ? codes : base + kLinStageBlocks * kLinATile, 1024u);
+    const uint32_t stage16 = a.stage_bytes >> 4;
+    const uint32_t rows16 = static_cast<uint32_t>(kFuse ? kLinFuseRows : a.box_rows) * 8u;
     // 32-channel steps of the tile's last stage
     const int last_steps = kb1 < a.Kb ? 4 * kLinStageBlocks : (a.Kb - 1) % kLinStageBlocks * 4 + a.last_ksteps;
     uint32_t s = 0, p = 0, g = 0, gp = 0, c = 0, cp = 0;
@@ -638,8 +767,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
       uint32_t acc = 0;  // the tile's first MMA overwrites the accumulator
       for (int kb = kb0; kb < kb1; kb += kLinStageBlocks) {
-        const bool last = kb + kLinStageBlocks >= kb1, first_half = (kb & 3) == 0, group_end = !first_half || last;
-        if ((first_half || kb == kb0) && !sf_ready && !(ok = wait(sf_full + 8 * g, gp))) break;
+        // a scale word serves two stages (kFuse: all are there, and stay, from the first on)
+        const bool last = kb + kLinStageBlocks >= kb1, first_half = (kb & 3) == 0;
+        const bool group_end = !kFuse && (!first_half || last);
+        if ((kb == kb0 || (!kFuse && first_half)) && !sf_ready && !(ok = wait(sf_full + 8 * g, gp))) break;
         if (!full_ready && !(ok = wait(full + 8 * s, p))) break;
         tc_fence_after();
         const uint32_t ns = s + 1 == static_cast<uint32_t>(a.stages) ? 0u : s + 1, np = ns ? p : p ^ 1u;
@@ -649,8 +780,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           seen = mbar_test_wait(full + 8 * ns, np) ? 1 : 0;
           if (group_end) seen |= mbar_test_wait(sf_full + 8 * ng, ngp) ? 2 : 0;
         }
-        const uint64_t ad = ad0 + s * stage16, bd = bd0 + s * stage16;
-        const uint32_t sf = tmem_base + a.sf_col + g * kLinSfCols<kPair>;
+        const uint64_t ad = ad0 + s * stage16;
+        const uint64_t bd = kFuse ? bd0 + static_cast<uint32_t>(kb - kb0) * rows16 : bd0 + s * stage16;
+        const uint32_t sf = tmem_base + a.sf_col +
+                            (kFuse ? static_cast<uint32_t>((kb >> 2) - (kb0 >> 2)) : g) * kLinSfCols<kPair>;
         const uint32_t idesc = idesc_mxf8(128 * kCtas, static_cast<uint32_t>(t.n), first_half ? 0u : 2u);
         constexpr uint32_t kNextByte = (1u << 4) | (1u << 29);  // the second block's byte of the scale words
         const int steps = last ? last_steps : 4 * kLinStageBlocks;
@@ -695,7 +828,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_wait(drain_bar, 0, &dummy, limit, kErrTimeoutDrain);
     }
     __syncwarp();
-  } else if (warp >= 2 && warp < 2 + kLinScaleWarps) {
+  } else if (!kFuse && warp >= 2 && warp < 2 + kLinScaleWarps) {
     // -------------------------------------------------------------- scales
     // Group of four blocks: the weights' word (the same for all 128 channels)
     // into four columns, the rows' words into the next: row 32 j + l at lane l
@@ -860,23 +993,29 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (split) {
     cluster_sync();  // every CTA's sums are in its shared memory
     if (first_tile < total) {
-      // each CTA adds and writes its share of the tile's groups of 8 channels
+      // each CTA adds and writes its share of the tile's groups of 8 channels (sums of a CTA that gave up are whatever
+      // its ring holds: the error word says that the call's results are invalid)
       const LinTile t = tiles.at(first_tile);
       const int r = static_cast<int>(cluster_ctarank()), items = t.rows * (kFp8Block / 8);
       for (int i = items * r / a.split + static_cast<int>(threadIdx.x); i < items * (r + 1) / a.split; i += kLinThreads) {
         const int row = i / (kFp8Block / 8), ch = t.nb * kFp8Block + i % (kFp8Block / 8) * 8;
         if (ch >= a.N || !check_bounds(t.row0 + row < a.M)) continue;
-        float v[8] = {};
-        for (int k = 0; k < a.split; ++k) {
-          const uint32_t src = map_to_cta(base + static_cast<uint32_t>(i) * 32u, static_cast<uint32_t>(k));
-          float w[8];
+        float v[8];
 #pragma unroll
-          for (int j = 0; j < 8; j += 4)
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(w[j]), "=f"(w[j + 1]), "=f"(w[j + 2]), "=f"(w[j + 3])
-                         : "r"(src + static_cast<uint32_t>(j) * 4u));
+        for (int j = 0; j < 8; j += 4) {
+          float w[kLinMaxSplit][4];  // every CTA's four sums in flight at a time
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = k == 0 ? w[j] : v[j] + w[j];
+          for (int k = 0; k < kLinMaxSplit; ++k) {
+            if (k < a.split)
+              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(w[k][0]), "=f"(w[k][1]), "=f"(w[k][2]), "=f"(w[k][3])
+                           : "r"(map_to_cta(base + static_cast<uint32_t>(i * 32 + j * 4), static_cast<uint32_t>(k))));
+          }
+#pragma unroll
+          for (int k = 0; k < kLinMaxSplit; ++k)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (k < a.split) v[j + h] = k == 0 ? w[0][h] : v[j + h] + w[k][h];
         }
         const __nv_bfloat16* const be = a.bias ? a.bias + static_cast<int64_t>(t.e) * a.N + ch : nullptr;
         uint32_t u[4];
@@ -890,7 +1029,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         store_bf16x8(a.out + (t.row0 + row) * a.ldo + ch, make_uint4(u[0], u[1], u[2], u[3]), a.N - ch, a.vec_out != 0);
       }
     }
-    cluster_sync();  // no CTA leaves while another may still read its sums
+    // no CTA leaves while another may still read its sums: waited for at the very end
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   tc_fence_before();
   if (kPair) {
@@ -906,6 +1047,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     } else {
       tmem_dealloc(tmem_base, a.tmem_cols);
     }
+  }
+  if (split) {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
 }
 

@@ -584,7 +584,7 @@ constexpr int64_t kLinMaxRows = int64_t{1} << 30;      // rows of x in a call
 constexpr int64_t kLinMaxChannels = int64_t{1} << 20;  // N, K
 
 std::atomic<int32_t> g_lin_force[4] = {};  // NT, mode (1 single CTA, 2 CTA pair), split, cap on the CTAs; 0 = automatic
-bool g_lin_attr_set[kMaxDevices][2] = {};
+bool g_lin_attr_set[kMaxDevices][3] = {};
 int g_lin_max_clusters[kMaxDevices] = {0};
 
 // How a product is tiled.
@@ -620,7 +620,7 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
       const double tiles = spans * (pair ? ceil_div(nblk, 2) : nblk);
       const double n = std::min<double>(nt, std::ceil(rows / std::ceil(rows / nt) / 16) * 16);
       const double mma = pair ? std::max(72.0, 0.56 * n) : std::max(78.0, 0.9 * n);
-      for (int split = 1; split <= (pair ? 1 : 8); ++split) {
+      for (int split = 1; split <= (pair ? 1 : qvae::kLinMaxSplit); ++split) {
         if (split > stages || (forced && g_lin_force[2] && split != std::min<int64_t>(pair ? 1 : g_lin_force[2].load(), stages))) continue;
         // one tile to a cluster: what the offsets give at most must fit the device
         if (split > 1 && linear_tiles(E, M, nblk, grouped, pair, nt) * split > 2 * sms) continue;
@@ -702,19 +702,27 @@ int launch_fp8_quant(int64_t M, int64_t K, int op, const void* x, int64_t ldx, u
   return QVAE_OK;
 }
 
-// offsets null: one span of M rows.  early: the kernel before this one on the stream is the quantiser, which lets this
+// The bf16 rows of a product that quantises them itself.
+struct LinRows {
+  const void* x;
+  int64_t ldx;
+  bool silu;
+};
+
+// offsets null: one span of M rows.  rows: quantised by the product (xq and x_scale unused).  early: the kernel before this one on the stream is the quantiser, which lets this
 // one start only when all that came before it has finished.
 int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq, const uint32_t* x_scale,
                   const int32_t* offsets, const uint8_t* wq, const uint8_t* w_scale, const void* bias, void* out,
-                  int64_t ldo, cudaStream_t stream, bool early = false) {
+                  int64_t ldo, cudaStream_t stream, bool early = false, const LinRows* rows = nullptr) {
   int rc = check_linear(E, M, N, K);
   if (rc) return rc;
   if (M == 0) return QVAE_OK;
-  if (!xq || !x_scale || !wq || !w_scale || !out || ldo < N) return QVAE_ERR_ARG;
+  if ((!rows && (!xq || !x_scale)) || !wq || !w_scale || !out || ldo < N) return QVAE_ERR_ARG;
   if (ldo > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
   if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(wq) || !aligned16(w_scale) || !aligned2(bias) ||
       !aligned2(out))
     return QVAE_ERR_ALIGN;
+  const bool fuse = rows != nullptr;
   int dev, sms;
   if ((rc = current_device(&dev))) return rc;
   if ((rc = sm_count(dev, &sms))) return rc;
@@ -737,14 +745,23 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.tiles_n = plan.pair ? (a.nblk + 1) / 2 : a.nblk;
   a.box_rows = (a.NT / (plan.pair ? 2 : 1) + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
   a.stage_bytes = qvae::kLinStageBlocks * (qvae::kLinATile + static_cast<uint32_t>(a.box_rows) * 128u);
+  const int blocks = static_cast<int>(ceil_div(ceil_div(a.Kb, qvae::kLinStageBlocks), plan.split)) * qvae::kLinStageBlocks;
+  if (fuse) {
+    a.x = static_cast<const __nv_bfloat16*>(rows->x);
+    a.ldx = rows->ldx;
+    a.silu = rows->silu ? 1 : 0;
+    a.vec_x = aligned16(rows->x) && (rows->ldx % 8 == 0 || M == 1) && (!rows->silu || K % 8 == 0);
+    a.codes_bytes = static_cast<uint32_t>(blocks) * qvae::kLinFuseRows * qvae::kFp8Block;
+    a.stage_bytes = qvae::kLinStageBlocks * qvae::kLinATile;
+  }
   const uint32_t rest = 1024u + qvae::kLinEpiWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u +
-                        4u * static_cast<uint32_t>(3 * E + 1);
+                        4u * static_cast<uint32_t>(3 * E + 1) +
+                        (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
   // (clusters with one tile each may sit two to an SM)
   const uint32_t room = plan.split > 1 && plan.max_tiles * plan.split > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
   a.stages = std::min<int>(qvae::kLinMaxStages, (room - rest) / a.stage_bytes);
-  if (plan.split > 1) a.stages = std::min<int>(a.stages, ceil_div(ceil_div(a.Kb, qvae::kLinStageBlocks), plan.split));
-  // the ring also takes a split tile's sums
-  const uint32_t ring = std::max(a.stages * a.stage_bytes, plan.split > 1 ? a.NT * qvae::kFp8Block * 4u : 0u);
+  if (fuse || plan.split > 1) a.stages = std::min(a.stages, blocks / qvae::kLinStageBlocks);
+  const uint32_t ring = a.stages * a.stage_bytes;  // (also takes a split tile's sums: NT * 512 bytes, less than a stage)
   // Clusters wait for one another's CTAs, and a CTA for its TMEM: no two CTAs that can share an SM may want more than
   // its 512 columns.  A split CTA takes at most 256 and a third of the shared memory, so that two fit and three do not,
   // and none fits beside a CTA that takes more columns (those take 170 KB or more).
@@ -754,7 +771,8 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   const uint32_t sf_cols = plan.pair ? qvae::kLinSfCols<true> : qvae::kLinSfCols<false>;
   a.acc_cols = static_cast<uint32_t>(a.NT);
   a.sf_col = (plan.split > 1 ? 1 : 2) * a.acc_cols;
-  const uint32_t cols = std::max(a.sf_col + 2 * sf_cols, a.sf_col - a.acc_cols + (a.acc_cols + 31) / 32 * 32);
+  const uint32_t sf_sets = fuse ? static_cast<uint32_t>(blocks + 3) / 4 + 1 : 2u;  // (a part of K may start inside a group)
+  const uint32_t cols = std::max(a.sf_col + sf_sets * sf_cols, a.sf_col - a.acc_cols + (a.acc_cols + 31) / 32 * 32);
   a.tmem_cols = 32;
   while (a.tmem_cols < cols) a.tmem_cols <<= 1;
   a.vec_out = aligned16(out) && (ldo % 8 == 0 || M == 1);
@@ -766,8 +784,8 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.ldo = ldo;
   a.wait_limit_ns = g_wait_limit_ns;
 
-  CUtensorMap tmap_x, tmap_xs, tmap_w;
-  {
+  CUtensorMap tmap_x = {}, tmap_xs = {}, tmap_w;
+  if (!fuse) {
     const cuuint64_t dims[3] = {128u, static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(a.Kb)};
     const cuuint64_t strides[2] = {128u, static_cast<cuuint64_t>(M) * 128u};
     const cuuint32_t box[3] = {128u, static_cast<cuuint32_t>(a.box_rows), qvae::kLinStageBlocks};
@@ -783,10 +801,13 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     if ((rc = encode_map(&tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, dims, strides, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE)))
       return rc;
   }
-  const auto kernel = plan.pair ? qvae::linear_fp8_kernel<true> : qvae::linear_fp8_kernel<false>;
-  if (!g_lin_attr_set[dev][plan.pair]) {
+  const auto kernel = fuse        ? qvae::linear_fp8_kernel<false, true>
+                      : plan.pair ? qvae::linear_fp8_kernel<true, false>
+                                  : qvae::linear_fp8_kernel<false, false>;
+  bool& attr_set = g_lin_attr_set[dev][fuse ? 2 : plan.pair ? 1 : 0];
+  if (!attr_set) {
     QVAE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
-    g_lin_attr_set[dev][plan.pair] = true;
+    attr_set = true;
   }
   int grid = sms;
   if (plan.pair) {
@@ -795,13 +816,21 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   }
   if (const int cap = g_lin_force[3]) grid = std::min(grid, cap);
   grid = static_cast<int>(std::min<int64_t>(plan.max_tiles * ctas, std::max(grid / ctas, 1) * ctas));
-  if (plan.split > 1) grid = static_cast<int>(plan.max_tiles) * ctas;
+  if (fuse || plan.split > 1) grid = static_cast<int>(plan.max_tiles) * ctas;
   QVAE_CUDA(launch_dependent(kernel, dim3(grid), qvae::kLinThreads, smem, stream, ctas, tmap_x, tmap_xs, tmap_w,
                              a));
   return QVAE_OK;
 }
 
-// The layer from bf16 rows: the quantiser into the workspace, then the product.
+// Whether the product quantises its rows itself: few rows, one tile to a CTA, and a CTA's part of K in shared memory.
+bool quantises_itself(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms) {
+  const LinPlan plan = known_plan(E, M, N, K, grouped, sms);
+  return !plan.pair && plan.NT <= qvae::kLinFuseRows && plan.max_tiles * plan.split <= (plan.split > 1 ? 2 : 1) * sms &&
+         ceil_div(ceil_div(ceil_div(K, qvae::kFp8Block), qvae::kLinStageBlocks), plan.split) * qvae::kLinStageBlocks <=
+             qvae::kLinFuseBlocks;
+}
+
+// The layer from bf16 rows: one launch for few rows; else the quantiser into the workspace, then the product.
 int launch_linear_fused(int64_t E, int64_t M, int64_t N, int64_t K, int op, const void* x, int64_t ldx,
                         const int32_t* offsets, const uint8_t* wq, const uint8_t* w_scale, const void* bias, void* out,
                         int64_t ldo, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -815,6 +844,15 @@ int launch_linear_fused(int64_t E, int64_t M, int64_t N, int64_t K, int op, cons
   if (ldo > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
   if (!aligned16(wq) || !aligned16(w_scale) || !aligned2(bias) || !aligned2(out) || !aligned16(workspace))
     return QVAE_ERR_ALIGN;
+  const LinRows rows = {x, ldx, op == QVAE_FP8_SILU_MUL};
+  if (!x || ldx < (rows.silu ? 2 * K : K)) return QVAE_ERR_ARG;
+  if (ldx > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
+  if (!aligned2(x)) return QVAE_ERR_ALIGN;
+  int dev, sms;
+  if ((rc = current_device(&dev))) return rc;
+  if ((rc = sm_count(dev, &sms))) return rc;
+  if (quantises_itself(E, M, N, K, offsets != nullptr, sms))
+    return launch_linear(E, M, N, K, nullptr, nullptr, offsets, wq, w_scale, bias, out, ldo, stream, false, &rows);
   uint8_t* const xq = static_cast<uint8_t*>(workspace);
   uint32_t* const x_scale = reinterpret_cast<uint32_t*>(xq + round256(qvae_fp8_code_bytes(M, K)));
   if ((rc = launch_fp8_quant(M, K, op, x, ldx, xq, x_scale, stream))) return rc;
@@ -1320,7 +1358,8 @@ int qvae_set_fused_quant(int32_t on) {
 }
 
 int qvae_set_linear_tiling(int32_t NT, int32_t mode, int32_t split, int32_t max_ctas) {
-  if (NT < 0 || NT > qvae::kLinMaxNT<true> || NT % 16 || mode < 0 || mode > 2 || split < 0 || split > 8 || max_ctas < 0)
+  if (NT < 0 || NT > qvae::kLinMaxNT<true> || NT % 16 || mode < 0 || mode > 2 || split < 0 || split > qvae::kLinMaxSplit ||
+      max_ctas < 0)
     return QVAE_ERR_ARG;
   g_lin_force[0] = NT;
   g_lin_force[1] = mode;
