@@ -523,9 +523,9 @@ int qvae_set_conv_cta_limit(int32_t max_ctas);
  * 256 of a CTA pair.
  *   NT        a multiple of 16, <= 240 (single CTAs take at most 128)
  *   mode      1 = single CTAs, 2 = CTA pairs (cta_group::2)
- *   split     CTAs that share a tile along K, <= 8 (single CTAs; as many as
- *             there are pairs of 128-channel blocks at most, and only where all
- *             tiles' CTAs fit the device twice)
+ *   split     CTAs (or pairs) that share a tile along K, at most 8 CTAs and as
+ *             many as there are pairs of 128-channel blocks, and only where
+ *             all tiles' CTAs fit the device at a time
  *   max_ctas  cap on the CTAs of a launch (split 1)
  * Zero = automatic.  A forced value that a call's sizes do not allow is taken
  * as automatic for that call.

@@ -518,12 +518,16 @@ def test_every_tiling_gives_the_same_products(q, mode, nt, ctas):
         q.qvae_set_linear_tiling()
 
 
-@pytest.mark.parametrize("split", [2, 3, 5, 8])
-@pytest.mark.parametrize("nt", [16, 64, 128])
-def test_tiles_split_along_k(q, nt, split):
+@pytest.mark.parametrize("mode,split", [(1, 2), (1, 3), (1, 5), (1, 8), (2, 2), (2, 3), (2, 4)])
+@pytest.mark.parametrize("nt", [16, 64, 128, 240])
+def test_tiles_split_along_k(q, nt, mode, split):
+    if mode == 1 and nt > 128:
+        pytest.skip("single CTAs take at most 128 rows")
     try:
-        q.qvae_set_linear_tiling(nt, 1, split)
-        for m, n, k in ((1, 128, 2048), (1, 300, 4096), (16, 257, 1100), (37, 300, 2000), (100, 129, 4444)):
+        q.qvae_set_linear_tiling(nt, mode, split)
+        for m, n, k in ((1, 128, 2048), (1, 300, 4096), (16, 257, 1100), (37, 300, 2000), (100, 129, 4444), (230, 300, 1500)):
+            if -(-m // nt) <= 2 or nt > 16:
+                assert q.qvae_get_linear_tiling(0, m, n, k) == {"NT": nt, "mode": mode, "split": min(split, -(-k // 256))}
             x, w, b = rows(m, k, m), matrix((n, k), n), matrix((1, n), 3)[0]
             p = q.fp8_quantize_weights(w)
             out = q.linear_fp8_fused(x, p, b)

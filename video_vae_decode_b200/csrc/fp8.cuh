@@ -358,6 +358,7 @@ constexpr uint32_t kLinATile = kFp8Block * kFp8Block;  // bytes of one weight ti
 constexpr uint32_t kLinBars = 8 * (2 * kLinMaxStages + 4 + 4 + 1);
 // The variant that quantises its rows itself: rows of its tile and 128-channel blocks of its part of K, at most.
 constexpr int kLinFuseRows = 16, kLinFuseBlocks = 32;
+constexpr int kLinFuseItems = 64;  // rows times blocks: one pass of its warps
 constexpr uint32_t kLinFuseScales = (kLinFuseBlocks / 4 + 1) * kLinFuseRows * 4;  // its scale words (a part may start inside a group)
 constexpr uint32_t kLinEpiBuf = 2048;                  // an epilogue warp's 32 rows x 32 channels of bf16
 // Most rows of a tile: two accumulators and two sets of scale words (4 columns of weights', 1 per 32 rows) fit the 512
@@ -428,19 +429,19 @@ struct LinTiles {
 // issues the MMAs; loads and scale words of both are counted on its barriers,
 // and its commits arrive on the barriers of both.
 //
-// Split along K (single CTAs): where few rows leave too few tiles to read the
-// weights with every SM, a cluster of `split` CTAs takes one tile, each a part
-// of its K.  The sums of each are put in its shared memory, added in the order
+// Split along K: where few rows leave too few tiles for the SMs, a cluster of
+// `split` CTAs (or pairs) takes one tile, each a part of its K.  The sums of each are put in its shared memory, added in the order
 // of the ranks over distributed shared memory (no atomics: the same bits every
 // time, and no workspace), and written.
 //
 // kFuse (single CTAs, one tile each): the rows are bf16 and eight warps quantise
 // the CTA's part of them -- the codes, scales and outputs of the quantiser and
 // the product, in one launch.  Every CTA of a row does it again, so it is for
-// few rows (at most 16 to a tile).  It is done once, in front of the MMAs, while
-// the ring fills with weights, whose loads bound such calls: a stage at a time
-// beside the MMAs it measured slower than the two launches (its chain of
-// barriers took 2200 cycles a stage).
+// few rows: one pass of the warps.  (16 rows in several passes took 8000 cycles
+// or more behind the weights' loads: 14 us for 16 x 8192 x 4096, the two
+// launches 12.)  It is done once, in front of the MMAs, while the ring fills
+// with weights: a stage at a time beside the MMAs its chain of barriers took
+// 2200 cycles a stage.
 //
 // Launched as a programmatic dependent.  With `early` (the quantiser of the
 // same call in front) the first weights are loaded before its end is waited
@@ -471,15 +472,17 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = a.wait_limit_ns;
   constexpr int kCtas = kPair ? 2 : 1;
-  const uint32_t rank = kPair ? cluster_ctarank() : 0u;  // 0 = leader of the pair
+  const bool split = a.split > 1;
+  const uint32_t cta = kPair || split ? cluster_ctarank() : 0u;  // in the cluster
+  const uint32_t rank = cta % kCtas;                             // in the pair: 0 = its leader
+  const uint32_t lead_cta = cta - rank;
   const bool leader = rank == 0;
-  const bool split = !kPair && a.split > 1;
   const int first_tile = kPair || split ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
   const int tile_step = kPair || split ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
   // this CTA's blocks of K: whole stages
   int kb0 = 0, kb1 = a.Kb;
   if (split) {
-    const int r = static_cast<int>(cluster_ctarank()), stages = (a.Kb + kLinStageBlocks - 1) / kLinStageBlocks;
+    const int r = static_cast<int>(cta) / kCtas, stages = (a.Kb + kLinStageBlocks - 1) / kLinStageBlocks;
     kb0 = stages * r / a.split * kLinStageBlocks;
     kb1 = min(stages * (r + 1) / a.split * kLinStageBlocks, a.Kb);
   }
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     if (!check_bounds(bytes <= a.stage_bytes && wrow >= 0 && wrow < a.E * a.nblk * a.Kb && at < static_cast<uint32_t>(a.stages)))
       return;
     if (kPair) {
-      tma_load_2d_pair(dst, &tmap_w, map_to_cta(bar, 0), 0, wrow * kFp8Block);
+      tma_load_2d_pair(dst, &tmap_w, map_to_cta(bar, lead_cta), 0, wrow * kFp8Block);
     } else {
       tma_load_2d(dst, &tmap_w, bar, 0, wrow * kFp8Block);
     }
@@ -588,49 +591,51 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     // MMA's swizzled order and scale bytes in shared memory.  Then four of the
     // warps put the scale words into TMEM: row l's at lane l.
     const LinTile t = tiles.at(first_tile);
-    const int qw = warp - 2, sub = lane >> 3, col = lane & 7;
-    const int blocks = kb1 - kb0, items = t.rows * blocks;
-    constexpr int kWarps = kLinScaleWarps + kLinEpiWarps, kUnroll = 2;
-    for (int i0 = qw * 4; i0 < items; i0 += kUnroll * kWarps * 4) {
-      uint4 w[kUnroll][2], u[kUnroll][2];
+    const int sub = lane >> 3, col = lane & 7;
+    const int blocks = kb1 - kb0, items = t.rows * blocks;  // at most kLinFuseItems
+    constexpr int kWarps = kLinScaleWarps + kLinEpiWarps, kItems = kLinFuseItems / (kWarps * 4);
+    uint4 w[kItems][2], u[kItems][2];
 #pragma unroll
-      for (int r = 0; r < kUnroll; ++r) {
-        const int item = i0 + r * kWarps * 4 + sub;
-        const int row = item / blocks, b = item - row * blocks;
-        const int64_t k = static_cast<int64_t>(kb0 + b) * kFp8Block + col * 16;
-        const uint16_t* const src = reinterpret_cast<const uint16_t*>(a.x) + (t.row0 + row) * a.ldx;
+    for (int r = 0; r < kItems; ++r) {
+      const int item = (r * kWarps + warp - 2) * 4 + sub;
+      const int row = item / blocks, b = item - row * blocks;
+      const int64_t k = static_cast<int64_t>(kb0 + b) * kFp8Block + col * 16;
+      const uint16_t* const src = reinterpret_cast<const uint16_t*>(a.x) + (t.row0 + row) * a.ldx;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool in = item < items && k + 8 * h < a.K && check_bounds(t.row0 + row < a.M);
-          w[r][h] = u[r][h] = make_uint4(0u, 0u, 0u, 0u);
-          if (in) {
-            w[r][h] = a.vec_x ? load_bf16x8<true>(src, k + 8 * h, a.K) : load_bf16x8<false>(src, k + 8 * h, a.K);
-            if (a.silu)
-              u[r][h] = a.vec_x ? load_bf16x8<true>(src + a.K, k + 8 * h, a.K) : load_bf16x8<false>(src + a.K, k + 8 * h, a.K);
-          }
+      for (int h = 0; h < 2; ++h) {
+        w[r][h] = u[r][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (item < items && k + 8 * h < a.K && check_bounds(t.row0 + row < a.M)) {
+          w[r][h] = a.vec_x ? load_bf16x8<true>(src, k + 8 * h, a.K) : load_bf16x8<false>(src, k + 8 * h, a.K);
+          if (a.silu)
+            u[r][h] = a.vec_x ? load_bf16x8<true>(src + a.K, k + 8 * h, a.K) : load_bf16x8<false>(src + a.K, k + 8 * h, a.K);
         }
       }
+    }
+    // the weights' words: lane g holds group g's
+    uint32_t wword = 0;
+    const int kg0 = kb0 >> 2, kg1 = (kb1 + 3) >> 2;
+    if (kg0 + lane < kg1) wword = __ldcg(a.w_scale + static_cast<int64_t>(t.e * a.nblk + t.nb) * a.kgroups + kg0 + lane);
 #pragma unroll
-      for (int r = 0; r < kUnroll; ++r) {
-        const int item = i0 + r * kWarps * 4 + sub;
-        const int row = item / blocks, b = item - row * blocks;
-        float v[2][8];
-        uint32_t m = 0;
+    for (int r = 0; r < kItems; ++r) {
+      const int item = (r * kWarps + warp - 2) * 4 + sub;
+      const int row = item / blocks, b = item - row * blocks;
+      float v[2][8];
+      uint32_t m = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          widen_bf16x8(w[r][h], v[h]);
-          if (a.silu) {  // (zeros beyond K stay zeros)
-            float up[8];
-            widen_bf16x8(u[r][h], up);
+      for (int h = 0; h < 2; ++h) {
+        widen_bf16x8(w[r][h], v[h]);
+        if (a.silu) {  // (zeros beyond K stay zeros)
+          float up[8];
+          widen_bf16x8(u[r][h], up);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[h][j] = silu_mul(v[h][j], up[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[h][j]));
+          for (int j = 0; j < 8; ++j) v[h][j] = silu_mul(v[h][j], up[j]);
         }
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (item >= items) continue;
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[h][j]));
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      if (item < items) {
         const uint32_t byte = e8m0_of_amax(m);
         const float inv = e8m0_reciprocal(byte);
         const uint2 lo = e4m3x8(v[0], inv), hi = e4m3x8(v[1], inv);
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
         // byte (kb & 3) of word [group][row]
         const int kb = kb0 + b;
         if (col == 0)
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(scale_words + static_cast<uint32_t>((((kb >> 2) - (kb0 >> 2)) * kLinFuseRows + row) * 4 + (kb & 3))),
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(scale_words + static_cast<uint32_t>((((kb >> 2) - kg0) * kLinFuseRows + row) * 4 + (kb & 3))),
                        "r"(byte)
                        : "memory");
       }
@@ -650,16 +655,14 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     named_barrier_sync(1, 32 * kWarps);
     if (warp < 2 + kLinScaleWarps) {
       const uint32_t dst = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + a.sf_col;
-      const uint32_t* const ws = a.w_scale + static_cast<int64_t>(t.e * a.nblk + t.nb) * a.kgroups;
-      for (int kg = kb0 >> 2; kg < (kb1 + 3) >> 2; ++kg) {
-        const uint32_t g = static_cast<uint32_t>(kg - (kb0 >> 2));
-        uint32_t w[8] = {};
-        w[0] = w[1] = w[2] = w[3] = __ldcg(ws + kg);
+      for (int g = 0; g < kg1 - kg0; ++g) {
+        uint32_t sf[8] = {};
+        sf[0] = sf[1] = sf[2] = sf[3] = __shfl_sync(0xFFFFFFFFu, wword, g);
         asm volatile("ld.shared.u32 %0, [%1];"
-                     : "=r"(w[4])
-                     : "r"(scale_words + (g * kLinFuseRows + static_cast<uint32_t>(lane & (kLinFuseRows - 1))) * 4u));
-        tmem_st_x4(dst + g * kLinSfCols<kPair>, w);
-        tmem_st_x4(dst + g * kLinSfCols<kPair> + 4, w + 4);
+                     : "=r"(sf[4])
+                     : "r"(scale_words + static_cast<uint32_t>(g * kLinFuseRows + (lane & (kLinFuseRows - 1))) * 4u));
+        tmem_st_x4(dst + static_cast<uint32_t>(g) * kLinSfCols<kPair>, sf);
+        tmem_st_x4(dst + static_cast<uint32_t>(g) * kLinSfCols<kPair> + 4, sf + 4);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -700,7 +703,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
         if (check_bounds(t.row0 >= 0 && t.row0 < a.M)) {
           if (kFuse) {  // no codes to load
           } else if (kPair) {
-            const uint32_t lead = map_to_cta(bar, 0);
+            const uint32_t lead = map_to_cta(bar, lead_cta);
             if (whole) {
               tma_load_3d<true>(dst_x, &tmap_x, lead, 0, row, kb);
             } else {
@@ -745,7 +748,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     };
     auto commit = [&](uint32_t bar) {
       if (kPair) {
-        mma_commit_pair_multicast(bar, 0x3);
+        mma_commit_pair_multicast(bar, static_cast<uint16_t>(0x3u << lead_cta));
       } else {
         mma_commit(bar);
       }
@@ -879,7 +882,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
           // cluster scope, which also waits for the next words' loads and for everything else this warp has in
           // flight (it cost 15 % of the whole product: 237 against 205 us at 8192 x 8192 x 4096)
           if (kPair) {
-            mbar_arrive_remote(map_to_cta(sf_full + 8 * g, 0));
+            mbar_arrive_remote(map_to_cta(sf_full + 8 * g, lead_cta));
           } else {
             mbar_arrive(sf_full + 8 * g);
           }
@@ -896,7 +899,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     // conflicts) and written as 16-byte groups of 8 channels.
     const int q = warp & 3;
     const uint32_t buf = epi_stage + static_cast<uint32_t>(warp - 2 - kLinScaleWarps) * kLinEpiBuf;
-    const uint32_t empty_leader = kPair ? map_to_cta(acc_empty, 0) : acc_empty;
+    const uint32_t empty_leader = kPair ? map_to_cta(acc_empty, lead_cta) : acc_empty;
     // stmatrix: lane 8 i + j gives line 8 * step + j, group i
     const uint32_t st_line = static_cast<uint32_t>(lane & 7), st_grp = static_cast<uint32_t>(lane >> 3);
     const uint32_t st_addr = buf + st_line * 64u + ((st_grp ^ (st_line >> 1)) << 4);
@@ -906,7 +909,8 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     uint32_t c = 0, cp = 0;
     if (a.early) grid_dependency_wait();
     if (split && first_tile < total) {
-      // this CTA's sums into its ring (every stage has been read): [row][128 channels] of fp32
+      // this CTA's sums into its ring (every stage has been read): [row][128 channels] of fp32.  The tile's groups of 4
+      // channels are then added CTA by CTA (see below)
       const LinTile t = tiles.at(first_tile);
       int got = 1;
       if (lane == 0) got = mbar_wait(acc_full, 0, abort_flag, limit, kErrTimeoutEpilogue);
@@ -991,42 +995,62 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
 
   __syncwarp();
   if (split) {
-    cluster_sync();  // every CTA's sums are in its shared memory
-    if (first_tile < total) {
-      // each CTA adds and writes its share of the tile's groups of 8 channels (sums of a CTA that gave up are whatever
-      // its ring holds: the error word says that the call's results are invalid)
-      const LinTile t = tiles.at(first_tile);
-      const int r = static_cast<int>(cluster_ctarank()), items = t.rows * (kFp8Block / 8);
-      for (int i = items * r / a.split + static_cast<int>(threadIdx.x); i < items * (r + 1) / a.split; i += kLinThreads) {
-        const int row = i / (kFp8Block / 8), ch = t.nb * kFp8Block + i % (kFp8Block / 8) * 8;
-        if (ch >= a.N || !check_bounds(t.row0 + row < a.M)) continue;
-        float v[8];
+    // Each CTA adds and writes its share of the tile's groups of 4 channels (sums of a CTA that gave up are whatever its
+    // ring holds: the error word says that the call's results are invalid).
+    const bool have = first_tile < total;
+    LinTile t = {};
+    if (have) t = tiles.at(first_tile);
+    const int r = static_cast<int>(cta) / kCtas, items = t.rows * (kFp8Block / 4);
+    const int end = items * (r + 1) / a.split, c0 = (t.nb * kCtas + static_cast<int>(rank)) * kFp8Block;
+    int i = items * r / a.split + static_cast<int>(threadIdx.x);
+    const __nv_bfloat16* const be = a.bias ? a.bias + static_cast<int64_t>(t.e) * a.N : nullptr;
+    float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto load_bias = [&] {
+      const int ch = c0 + i % (kFp8Block / 4) * 4;
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          float w[kLinMaxSplit][4];  // every CTA's four sums in flight at a time
+      for (int j = 0; j < 4; ++j)
+        if (be && ch + j < a.N) b[j] = __bfloat162float(be[ch + j]);
+    };
+    if (i < end) load_bias();  // (in flight while the others' sums are waited for)
+    cluster_sync();            // every CTA's sums are in its shared memory
+    for (; i < end; i += kLinThreads) {
+      const int row = i / (kFp8Block / 4), ch = c0 + i % (kFp8Block / 4) * 4;
+      float w[kLinMaxSplit][4];  // every CTA's sums in flight at a time
 #pragma unroll
-          for (int k = 0; k < kLinMaxSplit; ++k) {
-            if (k < a.split)
-              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(w[k][0]), "=f"(w[k][1]), "=f"(w[k][2]), "=f"(w[k][3])
-                           : "r"(map_to_cta(base + static_cast<uint32_t>(i * 32 + j * 4), static_cast<uint32_t>(k))));
-          }
+      for (int k = 0; k < kLinMaxSplit; ++k) {
+        // (beyond the split: the last one again, not used)
+        const uint32_t from = static_cast<uint32_t>(min(k, a.split - 1) * kCtas) + rank;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(w[k][0]), "=f"(w[k][1]), "=f"(w[k][2]), "=f"(w[k][3])
+                     : "r"(map_to_cta(base + static_cast<uint32_t>(i) * 16u, from)));
+        if (k + 1 == kLinMaxSplit / 2 && a.split <= kLinMaxSplit / 2) break;
+      }
+      float v[4];
 #pragma unroll
-          for (int k = 0; k < kLinMaxSplit; ++k)
+      for (int h = 0; h < 4; ++h) {
+        v[h] = w[0][h];
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-              if (k < a.split) v[j + h] = k == 0 ? w[0][h] : v[j + h] + w[k][h];
+        for (int k = 1; k < kLinMaxSplit; ++k)
+          if (k < a.split) v[h] += w[k][h];
+        v[h] += b[h];
+      }
+      if (ch < a.N && check_bounds(t.row0 + row < a.M)) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+        const uint2 u = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        __nv_bfloat16* const dst = a.out + (t.row0 + row) * a.ldo + ch;
+        if (a.vec_out && ch + 4 <= a.N) {
+          *reinterpret_cast<uint2*>(dst) = u;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (ch + j < a.N)
+              reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>((j < 2 ? u.x : u.y) >> ((j & 1) * 16));
         }
-        const __nv_bfloat16* const be = a.bias ? a.bias + static_cast<int64_t>(t.e) * a.N + ch : nullptr;
-        uint32_t u[4];
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float b0 = be && ch + j < a.N ? __bfloat162float(be[j]) : 0.0f;
-          const float b1 = be && ch + j + 1 < a.N ? __bfloat162float(be[j + 1]) : 0.0f;
-          const __nv_bfloat162 p2 = __floats2bfloat162_rn(v[j] + b0, v[j + 1] + b1);
-          u[j >> 1] = *reinterpret_cast<const uint32_t*>(&p2);
-        }
-        store_bf16x8(a.out + (t.row0 + row) * a.ldo + ch, make_uint4(u[0], u[1], u[2], u[3]), a.N - ch, a.vec_out != 0);
+      }
+      if (i + kLinThreads < end) {
+        i += kLinThreads;
+        load_bias();
+        i -= kLinThreads;
       }
     }
     // no CTA leaves while another may still read its sums: waited for at the very end

@@ -601,34 +601,44 @@ int64_t linear_tiles(int64_t E, int64_t M, int64_t nblk, bool grouped, bool pair
   return spans * (pair ? ceil_div(nblk, 2) : nblk);
 }
 
-// The tiling with the least estimated time, in SM cycles.  A launch takes waves of tiles, one to an SM (to two SMs: a
-// CTA pair); a tile takes its MMAs or the loads of its weights, whichever is longer, and what its epilogue leaves exposed.
+// The tiling with the least estimated time, in SM cycles.  A 32-channel step of a tile costs what shared memory moves
+// for it at 128 bytes a cycle -- 4 KB of weights in and out, n rows of 32 codes in and out (a pair: half of them to a
+// CTA) -- or the tensor cores' n / 2 cycles, whichever is longer (measured: 78 cycles at n = 16, 114 at 128, pairs 120 at
+// 240).  All SMs together read the weights at about 3300 bytes a cycle.  What a launch takes besides was measured on
+// small shapes: about 6000 cycles until the first MMA, an epilogue of 8 cycles a row, and for a split along K the sums'
+// way over distributed shared memory.
 LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms, bool forced = true) {
   const int64_t nblk = ceil_div(N, qvae::kFp8Block), Kb = ceil_div(K, qvae::kFp8Block);
   const int64_t stages = ceil_div(Kb, qvae::kLinStageBlocks);
   const int64_t busy = grouped ? std::min(E, M) : 1;     // experts that have rows, at most
   const double rows = static_cast<double>(M) / busy;     // of one of them
+  const double weights = static_cast<double>(busy) * nblk * Kb * qvae::kLinATile / 3300.0;
   LinPlan best = {};
   double least = 0;
   for (int mode = 1; mode <= 2; ++mode) {
     if (forced && g_lin_force[1] && mode != g_lin_force[1]) continue;
     const bool pair = mode == 2;
+    const int ctas = pair ? 2 : 1;
     const int most = pair ? qvae::kLinMaxNT<true> : qvae::kLinMaxNT<false>;
     for (int nt = 16; nt <= most; nt += 16) {
       if (forced && g_lin_force[0] && nt != std::min<int>(g_lin_force[0], most)) continue;
-      const double spans = busy * std::ceil(rows / nt);
-      const double tiles = spans * (pair ? ceil_div(nblk, 2) : nblk);
+      const int64_t max_tiles = linear_tiles(E, M, nblk, grouped, pair, nt);
+      const double tiles = busy * std::ceil(rows / nt) * ceil_div(nblk, ctas);
       const double n = std::min<double>(nt, std::ceil(rows / std::ceil(rows / nt) / 16) * 16);
-      const double mma = pair ? std::max(72.0, 0.56 * n) : std::max(78.0, 0.9 * n);
-      for (int split = 1; split <= (pair ? 1 : qvae::kLinMaxSplit); ++split) {
-        if (split > stages || (forced && g_lin_force[2] && split != std::min<int64_t>(pair ? 1 : g_lin_force[2].load(), stages))) continue;
-        // one tile to a cluster: what the offsets give at most must fit the device
-        if (split > 1 && linear_tiles(E, M, nblk, grouped, pair, nt) * split > 2 * sms) continue;
-        const double part = ceil_div(stages, split) * qvae::kLinStageBlocks * std::max(4 * mma, 420.0);
-        const double tile = part + 3000.0 + 4.0 * n + (split > 1 ? 1500.0 + 6.0 * n : 0.0);
-        const double time = std::ceil(tiles * split / (pair ? sms / 2 : sms)) * tile;
+      const double step = pair ? std::max(64 + n / 4, n / 2) : 64 + n / 2;
+      for (int split = 1; split * ctas <= qvae::kLinMaxSplit; ++split) {
+        if (split > stages || (forced && g_lin_force[2] && split != std::min<int64_t>(g_lin_force[2], stages))) continue;
+        // one tile to a cluster: what the offsets give at most must fit the device (small single CTAs: twice)
+        const bool twice = !pair && nt <= 32;
+        if (split > 1 && max_tiles * split * ctas > (twice ? 2 : 1) * sms) continue;
+        const double part = ceil_div(stages, split) * 4 * qvae::kLinStageBlocks * step, epilogue = 8 * n;
+        const double slots = split > 1 ? max_tiles * split : pair ? sms / 2 : sms;
+        const double waves = std::ceil(tiles * split / slots);
+        const double shared = split > 1 && max_tiles * split * ctas > sms ? 2 : 1;  // CTAs on an SM
+        const double time = 6000 + std::max(waves * part * shared, weights) + (waves - 1) * std::max(0.0, epilogue - part) +
+                            epilogue + (split > 1 ? 2500 + 8 * n : 0);
         if (!best.NT || time < least) {
-          best = {pair, nt, split, linear_tiles(E, M, nblk, grouped, pair, nt)};
+          best = {pair, nt, split, max_tiles};
           least = time;
         }
       }
@@ -738,7 +748,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.kgroups = (a.Kb + 3) / 4;
   const LinPlan plan = known_plan(E, M, N, K, offsets != nullptr, sms);
   if (plan.max_tiles > INT32_MAX / 2) return QVAE_ERR_SHAPE;
-  const int ctas = plan.pair ? 2 : plan.split;  // of a tile
+  const int ctas = (plan.pair ? 2 : 1) * plan.split;  // of a tile
   a.NT = plan.NT;
   a.split = plan.split;
   a.early = early ? 1 : 0;
@@ -758,15 +768,19 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
                         4u * static_cast<uint32_t>(3 * E + 1) +
                         (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
   // (clusters with one tile each may sit two to an SM)
-  const uint32_t room = plan.split > 1 && plan.max_tiles * plan.split > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
+  const uint32_t room = plan.split > 1 && plan.max_tiles * ctas > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
   a.stages = std::min<int>(qvae::kLinMaxStages, (room - rest) / a.stage_bytes);
-  if (fuse || plan.split > 1) a.stages = std::min(a.stages, blocks / qvae::kLinStageBlocks);
-  const uint32_t ring = a.stages * a.stage_bytes;  // (also takes a split tile's sums: NT * 512 bytes, less than a stage)
+  if (fuse || plan.split > 1) {  // as many as there are; a split tile's sums, NT * 512 bytes, take the ring's place
+    const int sums = plan.split > 1 ? static_cast<int>(ceil_div(a.NT * qvae::kFp8Block * 4, a.stage_bytes)) : 1;
+    a.stages = std::min(a.stages, std::max(blocks / qvae::kLinStageBlocks, sums));
+  }
+  const uint32_t ring = a.stages * a.stage_bytes;
   // Clusters wait for one another's CTAs, and a CTA for its TMEM: no two CTAs that can share an SM may want more than
   // its 512 columns.  A split CTA takes at most 256 and a third of the shared memory, so that two fit and three do not,
   // and none fits beside a CTA that takes more columns (those take 170 KB or more).
-  constexpr uint32_t kSplitSmem = 78 * 1024;
-  const uint32_t smem = std::max(rest + ring, plan.split > 1 ? kSplitSmem : 0u);
+  // (Split pairs take more than half of the shared memory.)
+  const uint32_t least = plan.split > 1 ? (plan.pair ? 116u : 78u) * 1024 : 0u;
+  const uint32_t smem = std::max(rest + ring, least);
   // two accumulators (a split CTA has one tile: one), read 32 columns at a time, and two sets of scale words
   const uint32_t sf_cols = plan.pair ? qvae::kLinSfCols<true> : qvae::kLinSfCols<false>;
   a.acc_cols = static_cast<uint32_t>(a.NT);
@@ -810,13 +824,16 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     attr_set = true;
   }
   int grid = sms;
-  if (plan.pair) {
-    if ((rc = max_pairs(kernel, qvae::kLinThreads, sms, &g_lin_max_clusters[dev]))) return rc;
-    grid = 2 * g_lin_max_clusters[dev];
+  if (fuse || plan.split > 1) {
+    grid = static_cast<int>(plan.max_tiles) * ctas;  // one tile each
+  } else {
+    if (plan.pair) {
+      if ((rc = max_pairs(kernel, qvae::kLinThreads, sms, &g_lin_max_clusters[dev]))) return rc;
+      grid = 2 * g_lin_max_clusters[dev];
+    }
+    if (const int cap = g_lin_force[3]) grid = std::min(grid, cap);
+    grid = static_cast<int>(std::min<int64_t>(plan.max_tiles * ctas, std::max(grid / ctas, 1) * ctas));
   }
-  if (const int cap = g_lin_force[3]) grid = std::min(grid, cap);
-  grid = static_cast<int>(std::min<int64_t>(plan.max_tiles * ctas, std::max(grid / ctas, 1) * ctas));
-  if (fuse || plan.split > 1) grid = static_cast<int>(plan.max_tiles) * ctas;
   QVAE_CUDA(launch_dependent(kernel, dim3(grid), qvae::kLinThreads, smem, stream, ctas, tmap_x, tmap_xs, tmap_w,
                              a));
   return QVAE_OK;
@@ -825,9 +842,10 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
 // Whether the product quantises its rows itself: few rows, one tile to a CTA, and a CTA's part of K in shared memory.
 bool quantises_itself(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms) {
   const LinPlan plan = known_plan(E, M, N, K, grouped, sms);
+  const int64_t blocks =
+      ceil_div(ceil_div(ceil_div(K, qvae::kFp8Block), qvae::kLinStageBlocks), plan.split) * qvae::kLinStageBlocks;
   return !plan.pair && plan.NT <= qvae::kLinFuseRows && plan.max_tiles * plan.split <= (plan.split > 1 ? 2 : 1) * sms &&
-         ceil_div(ceil_div(ceil_div(K, qvae::kFp8Block), qvae::kLinStageBlocks), plan.split) * qvae::kLinStageBlocks <=
-             qvae::kLinFuseBlocks;
+         blocks <= qvae::kLinFuseBlocks && std::min<int64_t>(M, plan.NT) * blocks <= qvae::kLinFuseItems;
 }
 
 // The layer from bf16 rows: one launch for few rows; else the quantiser into the workspace, then the product.
