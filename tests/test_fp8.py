@@ -141,23 +141,20 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
         qvae.fp8_quant_act(x)
     with pytest.raises(ValueError):
         qvae.fp8_quantize_weights(x)
-    w = qvae.Fp8Weights(torch.zeros(16384, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8), 1, 128, 128)
     with pytest.raises(ValueError):
-        qvae.linear_fp8_fused(x, w)
-    with pytest.raises(ValueError):
-        qvae.linear_fp8(torch.zeros((1, 4, 128), dtype=torch.uint8), torch.zeros((1, 4), dtype=torch.int32), w)
+        qvae.Fp8Weights(torch.zeros(16384, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8), 1, 128, 128)
 
 
 def test_binding_checks_of_layouts():
     cpu = -1                                                            # what a CPU tensor says its device is
     x = torch.zeros((4, 256), dtype=torch.bfloat16)
-    assert qvae._row_stride(x[:, :128], 128, cpu, "x") == 256
-    assert qvae._row_stride(x[:1, :128], 128, cpu, "x") == 128          # one row: its stride says nothing
+    assert qvae._rows(x[:, :128], 128, cpu, "x") == (4, 256)
+    assert qvae._rows(x[:1, :128], 128, cpu, "x") == (1, 128)           # one row: its stride says nothing
     for bad in (x[:, ::2], x.t(), x[0].expand(4, 256), x[0], x.half()):
         with pytest.raises(ValueError):
-            qvae._row_stride(bad, bad.shape[-1], cpu, "x")
+            qvae._rows(bad, bad.shape[-1], cpu, "x")
     with pytest.raises(ValueError):
-        qvae._row_stride(x, 128, cpu, "x")
+        qvae._rows(x, 128, cpu, "x")
     with pytest.raises(ValueError):
         qvae._buffer(torch.zeros(3, dtype=torch.int64), torch.int32, 3, cpu, "offsets")
     with pytest.raises(ValueError):

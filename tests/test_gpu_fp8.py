@@ -475,7 +475,8 @@ def test_binding_refusals(q):
                  lambda: q.linear_fp8_grouped_fused(x, o.cpu(), p), lambda: q.linear_fp8_grouped_fused(x, None, p),
                  lambda: q.linear_fp8_grouped_fused(x, o, p, bias=torch.zeros(64, dtype=torch.bfloat16, device="cuda")),
                  lambda: q.linear_fp8(q.fp8_quant_act(x)[0], q.fp8_quant_act(x)[1][:, :3], one),
-                 lambda: q.linear_fp8_fused(x, one._replace(wq=one.wq[:-1]))):
+                 lambda: q.Fp8Weights(one.wq[:-1], one.w_scale, 1, 64, 96), lambda: q.Fp8Weights(one.wq, one.w_scale[:2], 1, 64, 96),
+                 lambda: q.linear_fp8_fused(x.cpu(), one), lambda: q.Fp8Weights(one.wq, one.w_scale.cpu(), 1, 64, 96)):
         with pytest.raises(ValueError):
             call()
     with pytest.raises(q.QvaeError) as e:

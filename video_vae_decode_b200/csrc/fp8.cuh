@@ -308,6 +308,18 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) 
       : "memory");
 }
 
+// 32 lanes x 16 columns (thread i: lane i), loaded when it returns.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Four 8 x 8 matrices of 16-bit values, transposed, to the rows whose addresses the lanes give (lane 8 i + j: row j of
 // matrix i): thread l's word i goes to rows 2 (l % 4) and the next, column l / 4, of matrix i.
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&w)[4]) {
@@ -347,7 +359,8 @@ struct LinArgs {
 };
 
 constexpr int kLinScaleWarps = 4, kLinEpiWarps = 4;
-constexpr int kLinThreads = 32 * (2 + kLinScaleWarps + kLinEpiWarps);
+constexpr int kLinOutWarps = kLinScaleWarps + kLinEpiWarps;  // that write a CTA's only tile
+constexpr int kLinThreads = 32 * (2 + kLinOutWarps);
 constexpr int kLinMaxStages = 12;
 constexpr int kLinMaxExperts = 1024;
 constexpr int kLinMaxSplit = 8;                        // CTAs of a cluster that share a tile
@@ -447,7 +460,7 @@ struct LinTiles {
 // same call in front) the first weights are loaded before its end is waited
 // for; codes, scales and everything written wait for it.
 template <bool kPair, bool kFuse>
-__global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
+__global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_xs,
                       const __grid_constant__ CUtensorMap tmap_w, const LinArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -457,7 +470,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
   const uint32_t codes = base + static_cast<uint32_t>(a.stages) * a.stage_bytes;  // (kFuse) codes, then scale words
   const uint32_t scale_words = codes + a.codes_bytes;
   const uint32_t epi_stage = codes + (kFuse ? a.codes_bytes + kLinFuseScales : 0u);
-  const uint32_t bars = epi_stage + kLinEpiWarps * kLinEpiBuf;
+  const uint32_t bars = epi_stage + kLinOutWarps * kLinEpiBuf;
   const uint32_t full = bars, empty = full + 8 * kLinMaxStages;
   const uint32_t sf_full = empty + 8 * kLinMaxStages, sf_empty = sf_full + 16;
   const uint32_t acc_full = sf_empty + 16, acc_empty = acc_full + 16;
@@ -523,18 +536,6 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
   auto stage_bytes = [&](const LinTile& t) {
     return kLinStageBlocks * (kLinATile + (kFuse ? 0u : static_cast<uint32_t>(stage_boxes(t)) * (kLinBoxRows * 128u)));
   };
-  // A single layer's first tile is known: its weights are asked for before anything else is set up.
-  int ahead = kb0;  // (thread 0) blocks of the first tile whose weights have been asked for
-  if (!kPair && threadIdx.x == 0 && !a.offsets) {
-    if (!a.early) grid_dependency_wait();
-    const int spans = (a.M + a.NT - 1) / a.NT;
-    if (first_tile < spans * a.tiles_n) {
-      const LinTile t = lin_tile(first_tile, spans, a.tiles_n, 0, 0, a.M);
-      for (uint32_t i = 0; i < static_cast<uint32_t>(a.stages) && ahead < kb1; ++i, ahead += kLinStageBlocks)
-        load_w(i, t.nb * a.Kb + ahead, stage_bytes(t));
-    }
-  }
-  __syncwarp();
   if (warp == 1) {
     if (kPair) {
       tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), a.tmem_cols);
@@ -570,6 +571,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     }
     if (lane == 0) first[0] = 0;
   }
+  __syncwarp();
   tc_fence_before();
   if (kPair) {
     cluster_sync();  // both CTAs' barriers exist before either signals the other
@@ -583,6 +585,8 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
   const uint32_t tmem_base = *tmem_slot;
   LinTiles tiles{first, start, count, a.E, a.tiles_n};
   const int total = tiles.total();
+  // Where no CTA has a second tile, the scale warps, which have nothing left to do by then, write half of the outputs.
+  const bool solo = a.NT > 32 && (split || total <= tile_step);
 
   if (kFuse && warp >= 2 && first_tile < total) {
     // ----------------------------------------------------------- quantisers
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     const LinTile t = tiles.at(first_tile);
     const int sub = lane >> 3, col = lane & 7;
     const int blocks = kb1 - kb0, items = t.rows * blocks;  // at most kLinFuseItems
-    constexpr int kWarps = kLinScaleWarps + kLinEpiWarps, kItems = kLinFuseItems / (kWarps * 4);
+    constexpr int kWarps = kLinOutWarps, kItems = kLinFuseItems / (kWarps * 4);
     uint4 w[kItems][2], u[kItems][2];
 #pragma unroll
     for (int r = 0; r < kItems; ++r) {
@@ -675,6 +679,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     // ------------------------------------------------------------ producer
     uint32_t s = 0, p = 0, armed = 0, par = 0;
     bool waited = !a.early;
+    int ahead = kb0;  // blocks of the first tile whose weights have been asked for
     for (int tile = first_tile; tile < total; tile += tile_step) {
       const LinTile t = tiles.at(tile);
       const int mine = t.n / kCtas;  // this CTA's rows of the codes
@@ -686,8 +691,7 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
       const int wrow = (t.e * a.nblk + nb) * a.Kb;
       const int row = t.row0 + static_cast<int>(rank) * mine;
       if (!waited) {  // the ring is empty: fill it with weights, then wait for the rows' codes
-        for (uint32_t i = (ahead - kb0) / kLinStageBlocks; i < static_cast<uint32_t>(a.stages) && ahead < kb1;
-             ++i, ahead += kLinStageBlocks)
+        for (uint32_t i = 0; i < static_cast<uint32_t>(a.stages) && ahead < kb1; ++i, ahead += kLinStageBlocks)
           load_w(i, wrow + ahead, bytes);
         grid_dependency_wait();
         waited = true;
@@ -838,6 +842,8 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     // of column j.
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
     constexpr int kRowCols = kLinSfCols<kPair> - 4;
+    const int kg0 = kb0 >> 2, kg1 = (kb1 + 3) >> 2;
+    uint32_t next[1 + kRowCols];  // the next group's words, in flight while this group's are waited for
     if (a.early) {
       grid_dependency_wait();
       grid_dependents_launch();
@@ -848,7 +854,6 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
       const LinTile t = tiles.at(tile);
       const int nb = min(t.nb * kCtas + static_cast<int>(rank), a.nblk - 1);
       const uint32_t* const ws = a.w_scale + static_cast<int64_t>(t.e * a.nblk + nb) * a.kgroups;
-      uint32_t next[1 + kRowCols];  // the next group's words, in flight while this group's are waited for
       auto load = [&](int kg) {
         next[0] = __ldcg(ws + kg);
 #pragma unroll
@@ -858,7 +863,6 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
               32 * j < t.n && row < a.M ? __ldcg(a.x_scale + static_cast<int64_t>(kg) * a.M + row) : 0x7F7F7F7Fu;
         }
       };
-      const int kg0 = kb0 >> 2, kg1 = (kb1 + 3) >> 2;
       load(kg0);
       for (int kg = kg0; kg < kg1; ++kg) {
         uint32_t w[4 + kRowCols];
@@ -891,14 +895,17 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
         gp ^= g == 0;
       }
     }
-  } else if (warp >= 2 + kLinScaleWarps) {
+  }
+  if (warp >= (solo ? 2 : 2 + kLinScaleWarps)) {
     // ------------------------------------------------------------ epilogue
     // 32 rows of x (columns) by this warp's 32 channels (lanes) at a time:
     // sums + bias, rounded to bf16, transposed through shared memory (64-byte
     // lines of 32 channels, 16-byte groups permuted by the line against bank
     // conflicts) and written as 16-byte groups of 8 channels.
     const int q = warp & 3;
-    const uint32_t buf = epi_stage + static_cast<uint32_t>(warp - 2 - kLinScaleWarps) * kLinEpiBuf;
+    // blocks of 32 rows: all, or every other one (the scale warps': the odd ones)
+    const int r_first = solo && warp < 2 + kLinScaleWarps ? 32 : 0, r_step = solo ? 64 : 32;
+    const uint32_t buf = epi_stage + static_cast<uint32_t>(warp - 2) * kLinEpiBuf;
     const uint32_t empty_leader = kPair ? map_to_cta(acc_empty, lead_cta) : acc_empty;
     // stmatrix: lane 8 i + j gives line 8 * step + j, group i
     const uint32_t st_line = static_cast<uint32_t>(lane & 7), st_grp = static_cast<uint32_t>(lane >> 3);
@@ -917,16 +924,14 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
       if (__shfl_sync(0xFFFFFFFFu, got, 0)) {
         __syncwarp();
         tc_fence_after();
-        for (int r0 = 0; r0 < t.rows; r0 += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(r0), v);
-          tmem_ld_wait(v);
+#pragma unroll 1
+        for (int r0 = r_first / 2; r0 < t.n; r0 += r_step / 2) {  // (the ring holds NT rows, a multiple of 16)
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(r0), v);
+          const uint32_t dst = base + static_cast<uint32_t>(r0 * kFp8Block + q * 32 + lane) * 4u;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (r0 + j < t.rows)
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + static_cast<uint32_t>((r0 + j) * kFp8Block + q * 32 + lane) * 4u),
-                           "r"(v[j])
-                           : "memory");
+          for (int j = 0; j < 16; ++j)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(j * kFp8Block * 4)), "r"(v[j]) : "memory");
         }
         tc_fence_before();
       }
@@ -948,11 +953,11 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
       tc_fence_after();
       const uint32_t src = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c * a.acc_cols;
       const int ch = ch0 + 8 * static_cast<int>(ld_grp);  // the group of channels this lane writes
-      for (int r0 = 0; r0 < t.rows; r0 += 32) {
-        uint32_t v[32];
+      auto issue = [&](int r0, uint32_t(&v)[32]) {
         tmem_ld_16x256b_x4(src + static_cast<uint32_t>(r0), v);
         tmem_ld_16x256b_x4(src + (16u << 16) + static_cast<uint32_t>(r0), v + 16);
-        tmem_ld_wait(v);
+      };
+      auto process = [&](int r0, const uint32_t(&v)[32]) {
         __syncwarp();  // the last block's lines have been read
 #pragma unroll
         for (int step = 0; step < 4; ++step) {  // 8 rows of x: matrices of channels 0-7, 8-15, 16-23, 24-31
@@ -978,6 +983,12 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
             store_bf16x8(a.out + (t.row0 + r) * a.ldo + ch, w, a.N - ch, a.vec_out != 0);
           }
         }
+      };
+      for (int r0 = r_first; r0 < t.rows; r0 += r_step) {
+        uint32_t v[32];
+        issue(r0, v);
+        tmem_ld_wait(v);
+        process(r0, v);
       }
       tc_fence_before();
       __syncwarp();
@@ -1002,56 +1013,61 @@ __global__ void __launch_bounds__(kLinThreads, kFuse ? 2 : 1)
     if (have) t = tiles.at(first_tile);
     const int r = static_cast<int>(cta) / kCtas, items = t.rows * (kFp8Block / 4);
     const int end = items * (r + 1) / a.split, c0 = (t.nb * kCtas + static_cast<int>(rank)) * kFp8Block;
-    int i = items * r / a.split + static_cast<int>(threadIdx.x);
+    const int begin = items * r / a.split + static_cast<int>(threadIdx.x);
     const __nv_bfloat16* const be = a.bias ? a.bias + static_cast<int64_t>(t.e) * a.N : nullptr;
-    float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto load_bias = [&] {
-      const int ch = c0 + i % (kFp8Block / 4) * 4;
+    // kS: the split, rounded up to a power of two; eight loads of four sums in flight a thread
+    auto add = [&](auto KS) {
+      constexpr int kS = decltype(KS)::value, kU = kLinMaxSplit / kS;
+      for (int i0 = begin; i0 < end; i0 += kU * kLinThreads) {
+        float w[kU][kS][4], b[kU][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (be && ch + j < a.N) b[j] = __bfloat162float(be[ch + j]);
-    };
-    if (i < end) load_bias();  // (in flight while the others' sums are waited for)
-    cluster_sync();            // every CTA's sums are in its shared memory
-    for (; i < end; i += kLinThreads) {
-      const int row = i / (kFp8Block / 4), ch = c0 + i % (kFp8Block / 4) * 4;
-      float w[kLinMaxSplit][4];  // every CTA's sums in flight at a time
+        for (int u = 0; u < kU; ++u) {
+          const int i = min(i0 + u * kLinThreads, end - 1), ch = c0 + i % (kFp8Block / 4) * 4;
 #pragma unroll
-      for (int k = 0; k < kLinMaxSplit; ++k) {
-        // (beyond the split: the last one again, not used)
-        const uint32_t from = static_cast<uint32_t>(min(k, a.split - 1) * kCtas) + rank;
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(w[k][0]), "=f"(w[k][1]), "=f"(w[k][2]), "=f"(w[k][3])
-                     : "r"(map_to_cta(base + static_cast<uint32_t>(i) * 16u, from)));
-        if (k + 1 == kLinMaxSplit / 2 && a.split <= kLinMaxSplit / 2) break;
-      }
-      float v[4];
+          for (int k = 0; k < kS; ++k)  // (beyond the split: the last one again, not used)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(w[u][k][0]), "=f"(w[u][k][1]), "=f"(w[u][k][2]), "=f"(w[u][k][3])
+                         : "r"(map_to_cta(base + static_cast<uint32_t>(i) * 16u,
+                                          static_cast<uint32_t>(min(k, a.split - 1) * kCtas) + rank)));
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        v[h] = w[0][h];
+          for (int j = 0; j < 4; ++j) b[u][j] = be && ch + j < a.N ? __bfloat162float(be[ch + j]) : 0.0f;
+        }
 #pragma unroll
-        for (int k = 1; k < kLinMaxSplit; ++k)
-          if (k < a.split) v[h] += w[k][h];
-        v[h] += b[h];
-      }
-      if (ch < a.N && check_bounds(t.row0 + row < a.M)) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-        const uint2 u = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        __nv_bfloat16* const dst = a.out + (t.row0 + row) * a.ldo + ch;
-        if (a.vec_out && ch + 4 <= a.N) {
-          *reinterpret_cast<uint2*>(dst) = u;
-        } else {
+        for (int u = 0; u < kU; ++u) {
+          const int i = i0 + u * kLinThreads;
+          const int row = i / (kFp8Block / 4), ch = c0 + i % (kFp8Block / 4) * 4;
+          float v[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (ch + j < a.N)
-              reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>((j < 2 ? u.x : u.y) >> ((j & 1) * 16));
+          for (int h = 0; h < 4; ++h) {
+            v[h] = w[u][0][h];
+#pragma unroll
+            for (int k = 1; k < kS; ++k)
+              if (k < a.split) v[h] += w[u][k][h];
+            v[h] += b[u][h];
+          }
+          if (i < end && ch < a.N && check_bounds(t.row0 + row < a.M)) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+            const uint2 out = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            __nv_bfloat16* const dst = a.out + (t.row0 + row) * a.ldo + ch;
+            if (a.vec_out && ch + 4 <= a.N) {
+              *reinterpret_cast<uint2*>(dst) = out;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (ch + j < a.N)
+                  reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>((j < 2 ? out.x : out.y) >> ((j & 1) * 16));
+            }
+          }
         }
       }
-      if (i + kLinThreads < end) {
-        i += kLinThreads;
-        load_bias();
-        i -= kLinThreads;
-      }
+    };
+    cluster_sync();  // every CTA's sums are in its shared memory
+    if (a.split <= 2) {
+      add(IntC<2>{});
+    } else if (a.split <= 4) {
+      add(IntC<4>{});
+    } else {
+      add(IntC<8>{});
     }
     // no CTA leaves while another may still read its sums: waited for at the very end
     __syncwarp();

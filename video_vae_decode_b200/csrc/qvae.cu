@@ -604,15 +604,16 @@ int64_t linear_tiles(int64_t E, int64_t M, int64_t nblk, bool grouped, bool pair
 // The tiling with the least estimated time, in SM cycles.  A 32-channel step of a tile costs what shared memory moves
 // for it at 128 bytes a cycle -- 4 KB of weights in and out, n rows of 32 codes in and out (a pair: half of them to a
 // CTA) -- or the tensor cores' n / 2 cycles, whichever is longer (measured: 78 cycles at n = 16, 114 at 128, pairs 120 at
-// 240).  All SMs together read the weights at about 3300 bytes a cycle.  What a launch takes besides was measured on
-// small shapes: about 6000 cycles until the first MMA, an epilogue of 8 cycles a row, and for a split along K the sums'
-// way over distributed shared memory.
+// 240).  What a launch takes besides was measured on
+// small shapes: about 6000 cycles until the first MMA, an epilogue of 11 cycles a row (22 where half of the warps write
+// it beside the next tile), and for a split along K the sums'
+// way over distributed shared memory.  Weights come at 3300 bytes a cycle at most, and 30 to an SM.
 LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms, bool forced = true) {
   const int64_t nblk = ceil_div(N, qvae::kFp8Block), Kb = ceil_div(K, qvae::kFp8Block);
   const int64_t stages = ceil_div(Kb, qvae::kLinStageBlocks);
   const int64_t busy = grouped ? std::min(E, M) : 1;     // experts that have rows, at most
   const double rows = static_cast<double>(M) / busy;     // of one of them
-  const double weights = static_cast<double>(busy) * nblk * Kb * qvae::kLinATile / 3300.0;
+  const double weights = static_cast<double>(busy) * nblk * Kb * qvae::kLinATile;
   LinPlan best = {};
   double least = 0;
   for (int mode = 1; mode <= 2; ++mode) {
@@ -631,12 +632,14 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
         // one tile to a cluster: what the offsets give at most must fit the device (small single CTAs: twice)
         const bool twice = !pair && nt <= 32;
         if (split > 1 && max_tiles * split * ctas > (twice ? 2 : 1) * sms) continue;
-        const double part = ceil_div(stages, split) * 4 * qvae::kLinStageBlocks * step, epilogue = 8 * n;
+        const double part = ceil_div(stages, split) * 4 * qvae::kLinStageBlocks * step;
         const double slots = split > 1 ? max_tiles * split : pair ? sms / 2 : sms;
         const double waves = std::ceil(tiles * split / slots);
         const double shared = split > 1 && max_tiles * split * ctas > sms ? 2 : 1;  // CTAs on an SM
-        const double time = 6000 + std::max(waves * part * shared, weights) + (waves - 1) * std::max(0.0, epilogue - part) +
-                            epilogue + (split > 1 ? 2500 + 8 * n : 0);
+        const double reading = std::min<double>(sms, tiles * split * ctas);         // SMs
+        const double epilogue = 1300 + (waves > 1 ? 22 : 11) * n;
+        const double time = 6000 + std::max(waves * part * shared, weights / std::min(3300.0, 30 * reading)) +
+                            (waves - 1) * std::max(0.0, epilogue - part) + epilogue + (split > 1 ? 2700 + 200 * split + 15 * n : 0) + (pair ? 1500 : 0);
         if (!best.NT || time < least) {
           best = {pair, nt, split, max_tiles};
           least = time;
@@ -764,7 +767,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     a.codes_bytes = static_cast<uint32_t>(blocks) * qvae::kLinFuseRows * qvae::kFp8Block;
     a.stage_bytes = qvae::kLinStageBlocks * qvae::kLinATile;
   }
-  const uint32_t rest = 1024u + qvae::kLinEpiWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u +
+  const uint32_t rest = 1024u + qvae::kLinOutWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u +
                         4u * static_cast<uint32_t>(3 * E + 1) +
                         (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
   // (clusters with one tile each may sit two to an SM)

@@ -11,7 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import NamedTuple, Optional, Sequence
+from typing import Optional, Sequence
 
 import torch
 
@@ -445,13 +445,21 @@ def qvae_decode_layers(layers, workspace: torch.Tensor, stream=None) -> None:
 # current stream by default).  What a wrapper allocates is allocated on the
 # stream that the call runs on.
 
-class Fp8Weights(NamedTuple):
-    """Packed e4m3 weights of E matrices [N, K] (qvae_fp8_quantize_weights)."""
-    wq: torch.Tensor       # uint8, qvae_fp8_packed_weight_bytes(E, N, K)
-    w_scale: torch.Tensor  # uint8, qvae_fp8_weight_scale_bytes(E, N, K)
-    E: int
-    N: int
-    K: int
+class Fp8Weights:
+    """Packed e4m3 weights of E matrices [N, K] (qvae_fp8_quantize_weights): wq, uint8 of
+    qvae_fp8_packed_weight_bytes(E, N, K) bytes, and w_scale, uint8 of qvae_fp8_weight_scale_bytes(E, N, K).
+    Checked here, once; the tensors are not to be resized."""
+
+    __slots__ = ("wq", "w_scale", "E", "N", "K", "device")
+
+    def __init__(self, wq: torch.Tensor, w_scale: torch.Tensor, E: int, N: int, K: int):
+        self.wq, self.w_scale, self.E, self.N, self.K = wq, w_scale, int(E), int(N), int(K)
+        self.device = _device(wq, "wq")  # index
+        if self.E < 1 or self.N < 1 or self.K < 1:
+            raise ValueError("E, N and K are at least 1")
+        blocks = self.E * -(-self.N // 128)
+        _buffer(wq, torch.uint8, blocks * -(-self.K // 128) * 16384, self.device, "wq")
+        _buffer(w_scale, torch.uint8, blocks * -(-self.K // 512) * 4, self.device, "w_scale")
 
 
 def qvae_fp8_packed_weight_bytes(E: int, N: int, K: int) -> int:
@@ -481,14 +489,17 @@ def _buffer(t: torch.Tensor, dtype: torch.dtype, count: int, device: int, name: 
     return t.data_ptr()
 
 
-def _row_stride(t: torch.Tensor, columns: int, device: int, name: str) -> int:
-    """Elements between the rows of a bf16 matrix [M, columns] whose columns are adjacent."""
-    if t.dtype != torch.bfloat16 or t.get_device() != device or t.dim() != 2 or t.size(1) != columns:
-        raise ValueError(f"{name}: a bf16 matrix of {columns} columns on cuda:{device} is needed")
-    ld = t.stride(0) if t.size(0) > 1 else columns
-    if ld < columns or (columns > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: rows of adjacent columns that do not overlap are needed")
-    return ld
+def _rows(t: torch.Tensor, columns: int, device: int, name: str):
+    """(rows, elements between them) of a bf16 matrix whose columns are adjacent."""
+    if t.get_device() != device or t.dtype is not torch.bfloat16 or t.dim() != 2:
+        raise ValueError(f"{name}: a bf16 matrix on cuda:{device} is needed")
+    m, n = t.shape
+    ld, step = t.stride()
+    if m < 2:
+        ld = n  # (one row: its stride says nothing)
+    if n != columns or ld < n or (step != 1 and n > 1):
+        raise ValueError(f"{name}: rows of {columns} adjacent columns that do not overlap are needed")
+    return m, ld
 
 
 def _device(t: torch.Tensor, name: str) -> int:
@@ -554,9 +565,9 @@ def fp8_quant_act(x: torch.Tensor, silu_mul: bool = False, stream=None):
     device = _device(x, "x")
     if x.dim() != 2 or x.shape[1] < 1 or (silu_mul and x.shape[1] % 2):
         raise ValueError("x: a matrix is needed, with an even number of columns for silu_mul")
-    M, columns = x.shape
+    columns = x.shape[1]
     K = columns // 2 if silu_mul else columns
-    ld = _row_stride(x, columns, device, "x")
+    M, ld = _rows(x, columns, device, "x")
 
     def call(handle):
         xq = torch.empty((-(-K // 128), M, 128), dtype=torch.uint8, device=x.device)
@@ -569,51 +580,51 @@ def fp8_quant_act(x: torch.Tensor, silu_mul: bool = False, stream=None):
     return _run(device, stream, call)
 
 
-def _layer(device: int, weights: Fp8Weights, M: int, bias, out, offsets):
-    """Checks what every product takes; (row stride of out, addresses of weights, scales, bias, offsets)."""
-    wq, w_scale, E, N, K = weights
-    if offsets is None:
-        if E != 1:
-            raise ValueError(f"the weights hold {E} experts: use the grouped product")
-        po = None
-    else:
+def _layer(weights: Fp8Weights, M: int, bias, out, offsets):
+    """Checks what every product takes; (row stride of out, addresses of bias and offsets)."""
+    E, N, device = weights.E, weights.N, weights.device
+    po = pb = None
+    if offsets is not None:
         po = _buffer(offsets, torch.int32, E + 1, device, "offsets")
-    pb = None
+    elif E != 1:
+        raise ValueError(f"the weights hold {E} experts: use the grouped product")
     if bias is not None:
         if tuple(bias.shape) != (E, N) and (E != 1 or tuple(bias.shape) != (N,)):
             raise ValueError(f"bias: [N] or [E, N] is needed, N = {N}, E = {E}")
         pb = _buffer(bias, torch.bfloat16, E * N, device, "bias")
-    ldo = N
-    if out is not None:
-        ldo = _row_stride(out, N, device, "out")
-        if out.size(0) != M:
-            raise ValueError(f"out: {M} rows are needed")
-    blocks = E * -(-N // 128)
-    return (ldo, _buffer(wq, torch.uint8, blocks * -(-K // 128) * 16384, device, "weights.wq"),
-            _buffer(w_scale, torch.uint8, blocks * -(-K // 512) * 4, device, "weights.w_scale"), pb, po)
+    if out is None:
+        return N, pb, po
+    rows, ldo = _rows(out, N, device, "out")
+    if rows != M:
+        raise ValueError(f"out: {M} rows are needed")
+    return ldo, pb, po
+
+
+def _product_call(handle, name, xq, x_scale, weights, out, ldo, pb, po):
+    M, N = xq.shape[1], weights.N
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+    if po is None:
+        status = lib().qvae_linear_fp8(M, N, weights.K, xq.data_ptr(), x_scale.data_ptr(), weights.wq.data_ptr(),
+                                       weights.w_scale.data_ptr(), pb, out.data_ptr(), ldo, handle)
+    else:
+        status = lib().qvae_linear_fp8_grouped(weights.E, M, N, weights.K, xq.data_ptr(), x_scale.data_ptr(), po,
+                                               weights.wq.data_ptr(), weights.w_scale.data_ptr(), pb, out.data_ptr(),
+                                               ldo, handle)
+    if status:
+        _check(name, status)
+    return out
 
 
 def _product(name, xq, x_scale, weights, bias, out, offsets, stream):
-    device = _device(xq, "xq")
-    K = weights.K
+    K, device = weights.K, weights.device
     if xq.dim() != 3 or xq.shape[0] != -(-K // 128) or xq.shape[2] != 128:
         raise ValueError(f"xq: codes [{-(-K // 128)}, rows, 128] of {K} input channels are needed")
     M = xq.shape[1]
-    px = _buffer(xq, torch.uint8, xq.numel(), device, "xq")
-    ps = _buffer(x_scale, torch.int32, M * -(-K // 512), device, "x_scale")
-    ldo, pw, pws, pb, po = _layer(device, weights, M, bias, out, offsets)
-
-    def call(handle):
-        o = torch.empty((M, weights.N), dtype=torch.bfloat16, device=xq.device) if out is None else out
-        if po is None:
-            status = lib().qvae_linear_fp8(M, weights.N, K, px, ps, pw, pws, pb, o.data_ptr(), ldo, handle)
-        else:
-            status = lib().qvae_linear_fp8_grouped(weights.E, M, weights.N, K, px, ps, po, pw, pws, pb, o.data_ptr(),
-                                                   ldo, handle)
-        _check(name, status)
-        return o
-
-    return _run(device, stream, call)
+    _buffer(xq, torch.uint8, xq.numel(), device, "xq")
+    _buffer(x_scale, torch.int32, M * -(-K // 512), device, "x_scale")
+    ldo, pb, po = _layer(weights, M, bias, out, offsets)
+    return _run(device, stream, _product_call, name, xq, x_scale, weights, out, ldo, pb, po)
 
 
 def linear_fp8(xq: torch.Tensor, x_scale: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None,
@@ -632,19 +643,20 @@ def linear_fp8_grouped(xq: torch.Tensor, x_scale: torch.Tensor, offsets: torch.T
     return _product("qvae_linear_fp8_grouped", xq, x_scale, weights, bias, out, offsets, stream)
 
 
-def _fused_call(handle, name, x, ldx, weights, silu_mul, out, ldo, workspace, device, pw, pws, pb, po):
-    M, N, K = x.size(0), weights.N, weights.K
+def _fused_call(handle, name, x, M, ldx, weights, op, out, ldo, workspace, pb, po):
+    N, K, device = weights.N, weights.K, weights.device
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = fp8_workspace(M, K, x.device)
     pk = _buffer(workspace, torch.uint8, 0, device, "workspace")
-    op = QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN
     if po is None:
-        status = lib().qvae_linear_fp8_fused(M, N, K, op, x.data_ptr(), ldx, pw, pws, pb, out.data_ptr(), ldo, pk,
-                                             workspace.numel(), handle)
+        status = lib().qvae_linear_fp8_fused(M, N, K, op, x.data_ptr(), ldx, weights.wq.data_ptr(),
+                                             weights.w_scale.data_ptr(), pb, out.data_ptr(), ldo, pk, workspace.numel(),
+                                             handle)
     else:
-        status = lib().qvae_linear_fp8_grouped_fused(weights.E, M, N, K, op, x.data_ptr(), ldx, po, pw, pws, pb,
+        status = lib().qvae_linear_fp8_grouped_fused(weights.E, M, N, K, op, x.data_ptr(), ldx, po,
+                                                     weights.wq.data_ptr(), weights.w_scale.data_ptr(), pb,
                                                      out.data_ptr(), ldo, pk, workspace.numel(), handle)
     if status:
         _check(name, status)
@@ -652,10 +664,11 @@ def _fused_call(handle, name, x, ldx, weights, silu_mul, out, ldo, workspace, de
 
 
 def _fused(name, x, weights, bias, silu_mul, out, workspace, offsets, stream):
-    device = _device(x, "x")
-    ldx = _row_stride(x, 2 * weights.K if silu_mul else weights.K, device, "x")
-    ldo, pw, pws, pb, po = _layer(device, weights, x.size(0), bias, out, offsets)
-    return _run(device, stream, _fused_call, name, x, ldx, weights, silu_mul, out, ldo, workspace, device, pw, pws, pb, po)
+    device = weights.device
+    M, ldx = _rows(x, 2 * weights.K if silu_mul else weights.K, device, "x")
+    ldo, pb, po = _layer(weights, M, bias, out, offsets)
+    return _run(device, stream, _fused_call, name, x, M, ldx, weights, QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN,
+                out, ldo, workspace, pb, po)
 
 
 def linear_fp8_fused(x: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None, silu_mul: bool = False,
