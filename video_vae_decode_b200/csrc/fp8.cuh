@@ -365,8 +365,15 @@ constexpr int kLinMaxStages = 12;
 constexpr int kLinMaxExperts = 1024;
 constexpr int kLinMaxSplit = 8;                        // CTAs of a cluster that share a tile
 constexpr int kLinStageBlocks = 2;                     // 128-channel blocks of a pipeline stage
-constexpr int kLinBoxRows = 32;                        // rows of a small TMA box of codes
+constexpr int kLinBoxRows = 32;                        // TMA boxes of codes hold a multiple of these rows,
+constexpr int kLinBoxes = 4;                           // up to so many times as many
 constexpr int kLinSpanGroup = 16;                      // row spans walked under each output tile (see LinTiles)
+
+// Tensor maps: the codes in boxes of 32, 64, 96 and 128 rows of a stage's blocks, and the weights' tiles.
+struct LinMaps {
+  CUtensorMap x[kLinBoxes], w;
+};
+
 constexpr uint32_t kLinATile = kFp8Block * kFp8Block;  // bytes of one weight tile
 constexpr uint32_t kLinBars = 8 * (2 * kLinMaxStages + 4 + 4 + 1);
 // The variant that quantises its rows itself: rows of its tile and 128-channel blocks of its part of K, at most.
@@ -431,8 +438,9 @@ struct LinTiles {
 // the same time a stage from 32 rows to 240).
 //
 // Warp roles: warp 0 loads (a stage's weights as one 32 KB box that is already
-// in the MMA's order; its rows' codes as one box where they fill most of it,
-// else as boxes of 32 rows), warp 1 owns TMEM and issues the MMAs, warps 2-5 write the scale words of each group of four
+// in the MMA's order, its rows' codes as one box of the height that holds them:
+// a load takes the issuing thread about 100 cycles whatever its size, and boxes
+// of 32 rows bound ragged tiles), warp 1 owns TMEM and issues the MMAs, warps 2-5 write the scale words of each group of four
 // 128-channel blocks into TMEM (every lane quarter holds a copy: warp % 4 is
 // the quarter a warp can reach), warps 6-9 write the outputs.
 //
@@ -461,8 +469,7 @@ struct LinTiles {
 // for; codes, scales and everything written wait for it.
 template <bool kPair, bool kFuse>
 __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
-    linear_fp8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_xs,
-                      const __grid_constant__ CUtensorMap tmap_w, const LinArgs a) {
+    linear_fp8_kernel(const __grid_constant__ LinMaps maps, const LinArgs a) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -501,9 +508,8 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
   }
 
   if (threadIdx.x == 0) {
-    prefetch_tmap(&tmap_x);
-    prefetch_tmap(&tmap_xs);
-    prefetch_tmap(&tmap_w);
+    prefetch_tmap(&maps.w);
+    if (!kFuse) prefetch_tmap(&maps.x[a.box_rows / kLinBoxRows - 1]);
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
@@ -526,9 +532,9 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     if (!check_bounds(bytes <= a.stage_bytes && wrow >= 0 && wrow < a.E * a.nblk * a.Kb && at < static_cast<uint32_t>(a.stages)))
       return;
     if (kPair) {
-      tma_load_2d_pair(dst, &tmap_w, map_to_cta(bar, lead_cta), 0, wrow * kFp8Block);
+      tma_load_2d_pair(dst, &maps.w, map_to_cta(bar, lead_cta), 0, wrow * kFp8Block);
     } else {
-      tma_load_2d(dst, &tmap_w, bar, 0, wrow * kFp8Block);
+      tma_load_2d(dst, &maps.w, bar, 0, wrow * kFp8Block);
     }
   };
   // Bytes of a stage of tile t: the weights and the boxes of codes.
@@ -683,8 +689,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     for (int tile = first_tile; tile < total; tile += tile_step) {
       const LinTile t = tiles.at(tile);
       const int mine = t.n / kCtas;  // this CTA's rows of the codes
-      const int boxes = stage_boxes(t);
-      const bool whole = boxes * kLinBoxRows == a.box_rows;
+      const CUtensorMap* const map_x = &maps.x[stage_boxes(t) - 1];
       const uint32_t bytes = stage_bytes(t);
       // the second CTA of the last pair may have no output block of its own: it reads the last one again
       const int nb = min(t.nb * kCtas + static_cast<int>(rank), a.nblk - 1);
@@ -705,25 +710,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
           load_w(s, wrow + kb, bytes);
         }
         if (check_bounds(t.row0 >= 0 && t.row0 < a.M)) {
-          if (kFuse) {  // no codes to load
-          } else if (kPair) {
-            const uint32_t lead = map_to_cta(bar, lead_cta);
-            if (whole) {
-              tma_load_3d<true>(dst_x, &tmap_x, lead, 0, row, kb);
-            } else {
-              for (int i = 0; i < boxes * kLinStageBlocks; ++i)
-                tma_load_3d<true>(dst_x + (i % kLinStageBlocks) * (a.box_rows * 128) + i / kLinStageBlocks * (kLinBoxRows * 128),
-                                  &tmap_xs, lead, 0, row + i / kLinStageBlocks * kLinBoxRows, kb + i % kLinStageBlocks);
-            }
-          } else {
-            if (whole) {
-              tma_load_3d<false>(dst_x, &tmap_x, bar, 0, row, kb);
-            } else {
-              for (int i = 0; i < boxes * kLinStageBlocks; ++i)
-                tma_load_3d<false>(dst_x + (i % kLinStageBlocks) * (a.box_rows * 128) + i / kLinStageBlocks * (kLinBoxRows * 128),
-                                   &tmap_xs, bar, 0, row + i / kLinStageBlocks * kLinBoxRows, kb + i % kLinStageBlocks);
-            }
-          }
+          if (!kFuse) tma_load_3d<kPair>(dst_x, map_x, kPair ? map_to_cta(bar, lead_cta) : bar, 0, row, kb);
         }
         armed |= 1u << s;
         par = (par & ~(1u << s)) | (p << s);
@@ -760,7 +747,6 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     const uint64_t ad0 = sw128_kmajor_desc(base, 1024u);
     const uint64_t bd0 = sw128_kmajor_desc(kFuse ? codes : base + kLinStageBlocks * kLinATile, 1024u);
     const uint32_t stage16 = a.stage_bytes >> 4;
-    const uint32_t rows16 = static_cast<uint32_t>(kFuse ? kLinFuseRows : a.box_rows) * 8u;
     // 32-channel steps of the tile's last stage
     const int last_steps = kb1 < a.Kb ? 4 * kLinStageBlocks : (a.Kb - 1) % kLinStageBlocks * 4 + a.last_ksteps;
     uint32_t s = 0, p = 0, g = 0, gp = 0, c = 0, cp = 0;
@@ -773,6 +759,8 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
         break;
       }
       uint32_t acc = 0;  // the tile's first MMA overwrites the accumulator
+      // from the first block's codes to the second's
+      const uint32_t rows16 = static_cast<uint32_t>(kFuse ? kLinFuseRows : stage_boxes(t) * kLinBoxRows) * 8u;
       for (int kb = kb0; kb < kb1; kb += kLinStageBlocks) {
         // a scale word serves two stages (kFuse: all are there, and stay, from the first on)
         const bool last = kb + kLinStageBlocks >= kb1, first_half = (kb & 3) == 0;

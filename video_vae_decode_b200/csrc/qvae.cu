@@ -624,8 +624,10 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
     for (int nt = 16; nt <= most; nt += 16) {
       if (forced && g_lin_force[0] && nt != std::min<int>(g_lin_force[0], most)) continue;
       const int64_t max_tiles = linear_tiles(E, M, nblk, grouped, pair, nt);
-      const double tiles = busy * std::ceil(rows / nt) * ceil_div(nblk, ctas);
-      const double n = std::min<double>(nt, std::ceil(rows / std::ceil(rows / nt) / 16) * 16);
+      // spans of an expert: its rows are even for a single layer, anything around the mean otherwise
+      const double spans = !grouped ? std::ceil(rows / nt) : std::max(1.0, rows / nt + 0.5);
+      const double tiles = std::ceil(busy * spans) * ceil_div(nblk, ctas);
+      const double n = std::min<double>(nt, std::ceil(rows / spans / 16) * 16);
       const double step = pair ? std::max(64 + n / 4, n / 2) : 64 + n / 2;
       for (int split = 1; split * ctas <= qvae::kLinMaxSplit; ++split) {
         if (split > stages || (forced && g_lin_force[2] && split != std::min<int64_t>(g_lin_force[2], stages))) continue;
@@ -801,21 +803,21 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.ldo = ldo;
   a.wait_limit_ns = g_wait_limit_ns;
 
-  CUtensorMap tmap_x = {}, tmap_xs = {}, tmap_w;
+  qvae::LinMaps maps = {};
   if (!fuse) {
     const cuuint64_t dims[3] = {128u, static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(a.Kb)};
     const cuuint64_t strides[2] = {128u, static_cast<cuuint64_t>(M) * 128u};
-    const cuuint32_t box[3] = {128u, static_cast<cuuint32_t>(a.box_rows), qvae::kLinStageBlocks};
-    const cuuint32_t small[3] = {128u, qvae::kLinBoxRows, 1u};
-    if ((rc = encode_map(&tmap_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, dims, strides, box, 3, CU_TENSOR_MAP_SWIZZLE_128B)) ||
-        (rc = encode_map(&tmap_xs, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, dims, strides, small, 3, CU_TENSOR_MAP_SWIZZLE_128B)))
-      return rc;
+    for (int i = 0; i < a.box_rows / qvae::kLinBoxRows; ++i) {
+      const cuuint32_t box[3] = {128u, static_cast<cuuint32_t>((i + 1) * qvae::kLinBoxRows), qvae::kLinStageBlocks};
+      if ((rc = encode_map(&maps.x[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, dims, strides, box, 3, CU_TENSOR_MAP_SWIZZLE_128B)))
+        return rc;
+    }
   }
   {
     const cuuint64_t dims[2] = {128u, static_cast<cuuint64_t>(E) * a.nblk * a.Kb * qvae::kFp8Block};
     const cuuint64_t strides[1] = {128u};
     const cuuint32_t box[2] = {128u, qvae::kLinStageBlocks * qvae::kFp8Block};
-    if ((rc = encode_map(&tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, dims, strides, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE)))
+    if ((rc = encode_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, dims, strides, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE)))
       return rc;
   }
   const auto kernel = fuse        ? qvae::linear_fp8_kernel<false, true>
@@ -837,8 +839,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     if (const int cap = g_lin_force[3]) grid = std::min(grid, cap);
     grid = static_cast<int>(std::min<int64_t>(plan.max_tiles * ctas, std::max(grid / ctas, 1) * ctas));
   }
-  QVAE_CUDA(launch_dependent(kernel, dim3(grid), qvae::kLinThreads, smem, stream, ctas, tmap_x, tmap_xs, tmap_w,
-                             a));
+  QVAE_CUDA(launch_dependent(kernel, dim3(grid), qvae::kLinThreads, smem, stream, ctas, maps, a));
   return QVAE_OK;
 }
 
