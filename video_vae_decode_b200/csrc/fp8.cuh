@@ -268,6 +268,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
   }
 }
 
+// A whole warp's wait for a phase.  Mostly the phase is there, or comes within
+// the time that one try waits by itself: the warp then goes on without
+// diverging (one lane waiting and telling the others cost about 280 cycles
+// each time).  Else lane 0 waits within the time limit.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns,
+                                               int err_code) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, limit_ns, err_code);
+  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  __syncwarp();
+  return ok != 0;
+}
+
 // Eight bf16 values, or the first `left` of them; vec: dst is on 16 bytes.
 __device__ __forceinline__ void store_bf16x8(__nv_bfloat16* dst, const uint4& w, int left, bool vec) {
   if (vec && left >= 8) {
@@ -337,6 +351,7 @@ struct LinArgs {
   int nblk, kgroups;     // 128-channel output blocks; groups of four 128-channel blocks (one scale word)
   int tiles_n;           // output tiles: blocks, or pairs of them
   int NT;                // most rows of a tile (a multiple of 16)
+  int spans;             // spans of a single layer's rows
   int box_rows;          // rows of a CTA's part of a tile, rounded up to whole small boxes
   int stages;
   uint32_t stage_bytes;  // per 128-channel block of a stage: 16 KB of weights + box_rows rows of codes
@@ -507,22 +522,25 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     kb1 = min(stages * (r + 1) / a.split * kLinStageBlocks, a.Kb);
   }
 
-  if (threadIdx.x == 0) {
-    prefetch_tmap(&maps.w);
-    if (!kFuse) prefetch_tmap(&maps.x[a.box_rows / kLinBoxRows - 1]);
-    for (int i = 0; i < a.stages; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+  if (warp == 0) {
+    if (lane == 0) prefetch_tmap(&maps.w);
+    if (lane == 1 && !kFuse) prefetch_tmap(&maps.x[a.box_rows / kLinBoxRows - 1]);
+    if (lane < a.stages) {
+      mbar_init(full + 8 * lane, 1);
+      mbar_init(empty + 8 * lane, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(sf_full + 8 * i, kCtas * kLinScaleWarps);
-      mbar_init(sf_empty + 8 * i, 1);
-      mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_empty + 8 * i, kCtas * kLinEpiWarps);
+    if (lane < 2) {
+      mbar_init(sf_full + 8 * lane, kCtas * kLinScaleWarps);
+      mbar_init(sf_empty + 8 * lane, 1);
+      mbar_init(acc_full + 8 * lane, 1);
+      mbar_init(acc_empty + 8 * lane, kCtas * kLinEpiWarps);
     }
-    mbar_init(drain_bar, 1);
-    *abort_flag = 0;
+    if (lane == 2) {
+      mbar_init(drain_bar, 1);
+      *abort_flag = 0;
+    }
     fence_barrier_init();
+    __syncwarp();
   }
   // Weights of the stage at ring position `at`.  A last stage of one block loads what follows its weights, or the zeros
   // behind the tensor: no MMA reads it.
@@ -550,18 +568,21 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     }
   }
   if (!a.early) grid_dependency_wait();
-  if (warp == 2) {
+  if (!a.offsets) {
+    if (threadIdx.x == 64) {
+      first[0] = start[0] = 0;
+      first[1] = a.spans;
+      count[0] = a.M;
+    }
+  } else if (warp == 2) {
     // spans of each expert; an offset outside 0..M is clipped, one below an earlier one counts as that one
     int sum = 0, top = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      int lo = 0, hi = a.M;
-      if (a.offsets) {
-        lo = min(max(__ldcg(a.offsets + min(e, a.E)), top), a.M);
-        for (int o = 1; o < 32; o <<= 1) lo = max(lo, __shfl_up_sync(0xFFFFFFFFu, lo, o));
-        hi = max(lo, min(__ldcg(a.offsets + min(e + 1, a.E)), a.M));
-        top = __shfl_sync(0xFFFFFFFFu, hi, 31);
-      }
+      int lo = min(max(__ldcg(a.offsets + min(e, a.E)), top), a.M);
+      for (int o = 1; o < 32; o <<= 1) lo = max(lo, __shfl_up_sync(0xFFFFFFFFu, lo, o));
+      const int hi = max(lo, min(__ldcg(a.offsets + min(e + 1, a.E)), a.M));
+      top = __shfl_sync(0xFFFFFFFFu, hi, 31);
       const int c = e < a.E ? hi - lo : 0;
       int p = (c + a.NT - 1) / a.NT;
       for (int o = 1; o < 32; o <<= 1) {
@@ -726,16 +747,12 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     }
   } else if (warp == 1 && leader) {
     // ---------------------------------------------------------- MMA issuer
-    // The whole warp runs the loop; lane 0 waits, one elected lane issues a
+    // The whole warp runs the loop; one elected lane issues a
     // stage's MMAs and commits as straight-line code.  The barriers of the next
     // stage are probed before a stage is issued and the answer is read behind
     // it, so that a wait for something that is there already costs nothing.
-    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-      int ok = 1;
-      if (lane == 0) ok = mbar_wait(bar, parity, abort_flag, limit, kErrTimeoutMma);
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      __syncwarp();
-      return ok != 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      return mbar_wait_warp(bar, parity, abort_flag, limit, kErrTimeoutMma);
     };
     auto commit = [&](uint32_t bar) {
       if (kPair) {
@@ -858,10 +875,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
 #pragma unroll
         for (int j = 0; j < kRowCols; ++j) w[4 + j] = next[1 + j];
         if (kg + 1 < kg1) load(kg + 1);
-        int got = 1;
-        if (lane == 0) got = mbar_wait(sf_empty + 8 * g, gp ^ 1, abort_flag, limit, kErrTimeoutConvert);
-        if (!(ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0)) break;
-        __syncwarp();
+        if (!(ok = mbar_wait_warp(sf_empty + 8 * g, gp ^ 1, abort_flag, limit, kErrTimeoutConvert))) break;
         tc_fence_after();
         const uint32_t dst = tmem_base + quarter + a.sf_col + g * kLinSfCols<kPair>;
 #pragma unroll
@@ -907,10 +921,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
       // this CTA's sums into its ring (every stage has been read): [row][128 channels] of fp32.  The tile's groups of 4
       // channels are then added CTA by CTA (see below)
       const LinTile t = tiles.at(first_tile);
-      int got = 1;
-      if (lane == 0) got = mbar_wait(acc_full, 0, abort_flag, limit, kErrTimeoutEpilogue);
-      if (__shfl_sync(0xFFFFFFFFu, got, 0)) {
-        __syncwarp();
+      if (mbar_wait_warp(acc_full, 0, abort_flag, limit, kErrTimeoutEpilogue)) {
         tc_fence_after();
 #pragma unroll 1
         for (int r0 = r_first / 2; r0 < t.n; r0 += r_step / 2) {  // (the ring holds NT rows, a multiple of 16)
@@ -934,10 +945,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
         for (int i = 0; i < 4; ++i)
           if (ch0 + 8 * i + (lane >> 2) < a.N) b[i] = __bfloat162float(be[ch0 + 8 * i + (lane >> 2)]);
       }
-      int got = 1;
-      if (lane == 0) got = mbar_wait(acc_full + 8 * c, cp, abort_flag, limit, kErrTimeoutEpilogue);
-      if (!__shfl_sync(0xFFFFFFFFu, got, 0)) break;
-      __syncwarp();
+      if (!mbar_wait_warp(acc_full + 8 * c, cp, abort_flag, limit, kErrTimeoutEpilogue)) break;
       tc_fence_after();
       const uint32_t src = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c * a.acc_cols;
       const int ch = ch0 + 8 * static_cast<int>(ld_grp);  // the group of channels this lane writes

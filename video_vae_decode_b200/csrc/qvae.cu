@@ -755,6 +755,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   if (plan.max_tiles > INT32_MAX / 2) return QVAE_ERR_SHAPE;
   const int ctas = (plan.pair ? 2 : 1) * plan.split;  // of a tile
   a.NT = plan.NT;
+  a.spans = static_cast<int>(ceil_div(M, a.NT));
   a.split = plan.split;
   a.early = early ? 1 : 0;
   a.tiles_n = plan.pair ? (a.nblk + 1) / 2 : a.nblk;
