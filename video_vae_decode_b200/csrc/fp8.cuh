@@ -747,10 +747,8 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     }
   } else if (warp == 1 && leader) {
     // ---------------------------------------------------------- MMA issuer
-    // The whole warp runs the loop; one elected lane issues a
-    // stage's MMAs and commits as straight-line code.  The barriers of the next
-    // stage are probed before a stage is issued and the answer is read behind
-    // it, so that a wait for something that is there already costs nothing.
+    // The whole warp runs the loop; one elected lane issues a stage's MMAs and
+    // commits as straight-line code.
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return mbar_wait_warp(bar, parity, abort_flag, limit, kErrTimeoutMma);
     };
@@ -767,7 +765,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     // 32-channel steps of the tile's last stage
     const int last_steps = kb1 < a.Kb ? 4 * kLinStageBlocks : (a.Kb - 1) % kLinStageBlocks * 4 + a.last_ksteps;
     uint32_t s = 0, p = 0, g = 0, gp = 0, c = 0, cp = 0;
-    bool issued = false, ok = true, full_ready = false, sf_ready = false;
+    bool issued = false, ok = true;
     for (int tile = first_tile; tile < total && ok; tile += tile_step) {
       const LinTile t = tiles.at(tile);
       const uint32_t d = tmem_base + c * a.acc_cols;
@@ -782,16 +780,9 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
         // a scale word serves two stages (kFuse: all are there, and stay, from the first on)
         const bool last = kb + kLinStageBlocks >= kb1, first_half = (kb & 3) == 0;
         const bool group_end = !kFuse && (!first_half || last);
-        if ((kb == kb0 || (!kFuse && first_half)) && !sf_ready && !(ok = wait(sf_full + 8 * g, gp))) break;
-        if (!full_ready && !(ok = wait(full + 8 * s, p))) break;
+        if ((kb == kb0 || (!kFuse && first_half)) && !(ok = wait(sf_full + 8 * g, gp))) break;
+        if (!(ok = wait(full + 8 * s, p))) break;
         tc_fence_after();
-        const uint32_t ns = s + 1 == static_cast<uint32_t>(a.stages) ? 0u : s + 1, np = ns ? p : p ^ 1u;
-        const uint32_t ng = group_end ? g ^ 1u : g, ngp = group_end && g ? gp ^ 1u : gp;
-        int seen = 0;
-        if (lane == 0) {
-          seen = mbar_test_wait(full + 8 * ns, np) ? 1 : 0;
-          if (group_end) seen |= mbar_test_wait(sf_full + 8 * ng, ngp) ? 2 : 0;
-        }
         const uint64_t ad = ad0 + s * stage16;
         const uint64_t bd = kFuse ? bd0 + static_cast<uint32_t>(kb - kb0) * rows16 : bd0 + s * stage16;
         const uint32_t sf = tmem_base + a.sf_col +
@@ -818,13 +809,11 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
         __syncwarp();
         issued = true;
         acc = 1;
-        seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
-        full_ready = (seen & 1) != 0;
-        sf_ready = (seen & 2) != 0;
-        s = ns;
-        p = np;
-        g = ng;
-        gp = ngp;
+        if (++s == static_cast<uint32_t>(a.stages)) { s = 0; p ^= 1; }
+        if (group_end) {
+          g ^= 1;
+          gp ^= g == 0;
+        }
       }
       c ^= 1;
       cp ^= c == 0;
