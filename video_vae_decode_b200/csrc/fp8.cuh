@@ -352,6 +352,7 @@ struct LinArgs {
   int tiles_n;           // output tiles: blocks, or pairs of them
   int NT;                // most rows of a tile (a multiple of 16)
   int spans;             // spans of a single layer's rows
+  int span_group;        // spans walked under each output tile (see LinTiles)
   int box_rows;          // rows of a CTA's part of a tile, rounded up to whole small boxes
   int stages;
   uint32_t stage_bytes;  // per 128-channel block of a stage: 16 KB of weights + box_rows rows of codes
@@ -380,11 +381,10 @@ constexpr int kLinMaxStages = 12;
 constexpr int kLinMaxExperts = 1024;
 constexpr int kLinMaxSplit = 8;                        // CTAs of a cluster that share a tile
 constexpr int kLinStageBlocks = 2;                     // 128-channel blocks of a pipeline stage
-constexpr int kLinBoxRows = 32;                        // TMA boxes of codes hold a multiple of these rows,
-constexpr int kLinBoxes = 4;                           // up to so many times as many
-constexpr int kLinSpanGroup = 16;                      // row spans walked under each output tile (see LinTiles)
+constexpr int kLinBoxRows = 16;                        // TMA boxes of codes hold a multiple of these rows,
+constexpr int kLinBoxes = 8;                           // up to so many times as many
 
-// Tensor maps: the codes in boxes of 32, 64, 96 and 128 rows of a stage's blocks, and the weights' tiles.
+// Tensor maps: the codes in boxes of 16, 32 .. 128 rows of a stage's blocks, and the weights' tiles.
 struct LinMaps {
   CUtensorMap x[kLinBoxes], w;
 };
@@ -409,10 +409,10 @@ struct LinTile {
 };
 
 // Tile `local` of an expert's `count` rows from `start` in `spans` spans.
-__device__ __forceinline__ LinTile lin_tile(int local, int spans, int tiles_n, int e, int start, int count) {
-  const int full = kLinSpanGroup * tiles_n;
-  const int g0 = local / full * kLinSpanGroup, in = local % full;
-  const int gs = min(kLinSpanGroup, spans - g0);
+__device__ __forceinline__ LinTile lin_tile(int local, int spans, int group, int tiles_n, int e, int start, int count) {
+  const int full = group * tiles_n;
+  const int g0 = local / full * group, in = local % full;
+  const int gs = min(group, spans - g0);
   LinTile t;
   t.e = e;
   t.nb = in / gs;
@@ -429,16 +429,16 @@ __device__ __forceinline__ LinTile lin_tile(int local, int spans, int tiles_n, i
 // `first` [E + 1]: spans before expert e; `start` [E]: its first row; `count`
 // [E]: its rows.  Tiles are walked in increasing order, so the expert is found
 // by moving on from the last one.  Inside an expert the order is: groups of
-// kLinSpanGroup spans; output tiles; spans of the group -- what runs at one
-// time then shares both its weights and its rows out of L2.
+// `group` spans; output tiles; spans of the group -- what runs at one time then
+// shares its weights, and the group's codes stay in L2.
 struct LinTiles {
   const int *first, *start, *count;
-  int E, tiles_n;
+  int E, tiles_n, group;
   int e = 0;
   __device__ __forceinline__ int total() const { return first[E] * tiles_n; }
   __device__ __forceinline__ LinTile at(int tile) {
     while (tile >= first[e + 1] * tiles_n) ++e;
-    return lin_tile(tile - first[e] * tiles_n, first[e + 1] - first[e], tiles_n, e, start[e], count[e]);
+    return lin_tile(tile - first[e] * tiles_n, first[e + 1] - first[e], group, tiles_n, e, start[e], count[e]);
   }
 };
 
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
   // of this grid still waits for.
   if (!a.early) grid_dependents_launch();
   const uint32_t tmem_base = *tmem_slot;
-  LinTiles tiles{first, start, count, a.E, a.tiles_n};
+  LinTiles tiles{first, start, count, a.E, a.tiles_n, a.span_group};
   const int total = tiles.total();
   // Where no CTA has a second tile, the scale warps, which have nothing left to do by then, write half of the outputs.
   const bool solo = a.NT > 32 && (split || total <= tile_step);
