@@ -640,7 +640,8 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
         const double shared = split > 1 && max_tiles * split * ctas > sms ? 2 : 1;  // CTAs on an SM
         const double reading = std::min<double>(sms, tiles * split * ctas);         // SMs
         const double epilogue = 1300 + (waves > 1 ? 22 : 11) * n;
-        const double time = 6000 + std::max(waves * part * shared, weights / std::min(3300.0, 30 * reading)) +
+        const double steps = waves * part * shared, bytes = weights / std::min(3300.0, 30 * reading);
+        const double time = 6000 + std::max(steps, bytes) + 0.25 * std::min(steps, bytes) +
                             (waves - 1) * std::max(0.0, epilogue - part) + epilogue + (split > 1 ? 2700 + 200 * split + 15 * n : 0) + (pair ? 1500 : 0);
         if (!best.NT || time < least) {
           best = {pair, nt, split, max_tiles};
