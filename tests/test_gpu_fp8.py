@@ -585,3 +585,25 @@ def test_few_rows_quantised_by_the_product(q, m, n, k, extra, split, silu):
         fine = [i for i in range(m) if not (m > 4 and i == 2)]
         y, s = ref.linear(ref.act_values(x[fine]), ref.weight_values(w), b)
         check_product(one[fine], y, s, k)
+
+
+@pytest.mark.parametrize("m,n,k,split", [(1, 4096, 4096, 0), (2, 6000, 4096, 2), (2, 128, 8192, 2), (4, 4096, 8192, 0), (1, 18944, 4096, 0),
+                                         (2, 2048, 16384, 8)])
+def test_few_rows_of_many_experts_and_large_layers(q, m, n, k, split):
+    # what the variants keep in shared memory besides their ring: the table of 1024 experts, codes of a long part of K
+    x = rows(m, k, 1)
+    try:
+        q.qvae_set_linear_tiling(16 if split else 0, 1 if split else 0, split)
+        w = matrix((n, k), 2)
+        p = q.fp8_quantize_weights(w)
+        y, s = ref.linear(ref.act_values(x), ref.weight_values(w))
+        check_product(q.linear_fp8_fused(x, p), y, s, k)
+        many = q.Fp8Weights(p.wq.repeat(1024) if n * k < 1 << 21 else p.wq, p.w_scale.repeat(1024) if n * k < 1 << 21 else p.w_scale,
+                            1024 if n * k < 1 << 21 else 1, n, k)
+        if many.E > 1:
+            o = torch.full((1025,), m, dtype=torch.int32, device="cuda")
+            o[:700] = 0
+            check_product(q.linear_fp8_grouped_fused(x, o, many), y, s, k)
+        assert q.qvae_get_error() == 0
+    finally:
+        q.qvae_set_linear_tiling()

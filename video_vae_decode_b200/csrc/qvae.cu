@@ -718,6 +718,11 @@ int launch_fp8_quant(int64_t M, int64_t K, int op, const void* x, int64_t ldx, u
   return QVAE_OK;
 }
 
+// Shared memory of a product besides its ring: alignment, staging of the outputs, barriers, the table of tiles.
+uint32_t linear_smem_besides_ring(int64_t E) {
+  return 1024u + qvae::kLinOutWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u + 4u * static_cast<uint32_t>(3 * E + 1);
+}
+
 // The bf16 rows of a product that quantises them itself.
 struct LinRows {
   const void* x;
@@ -774,9 +779,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     a.codes_bytes = static_cast<uint32_t>(blocks) * qvae::kLinFuseRows * qvae::kFp8Block;
     a.stage_bytes = qvae::kLinStageBlocks * qvae::kLinATile;
   }
-  const uint32_t rest = 1024u + qvae::kLinOutWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u +
-                        4u * static_cast<uint32_t>(3 * E + 1) +
-                        (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
+  const uint32_t rest = linear_smem_besides_ring(E) + (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
   // (clusters with one tile each may sit two to an SM)
   const uint32_t room = plan.split > 1 && plan.max_tiles * ctas > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
   a.stages = std::min<int>(qvae::kLinMaxStages, (room - rest) / a.stage_bytes);
@@ -785,6 +788,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     a.stages = std::min(a.stages, std::max(blocks / qvae::kLinStageBlocks, sums));
   }
   const uint32_t ring = a.stages * a.stage_bytes;
+  if (a.stages < 1 || (plan.split > 1 && ring < a.NT * qvae::kFp8Block * 4u)) return QVAE_ERR_UNSUPPORTED;
   // Clusters wait for one another's CTAs, and a CTA for its TMEM: no two CTAs that can share an SM may want more than
   // its 512 columns.  A split CTA takes at most 256 and a third of the shared memory, so that two fit and three do not,
   // and none fits beside a CTA that takes more columns (those take 170 KB or more).
@@ -853,8 +857,12 @@ bool quantises_itself(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, 
   const LinPlan plan = known_plan(E, M, N, K, grouped, sms);
   const int64_t blocks =
       ceil_div(ceil_div(ceil_div(K, qvae::kFp8Block), qvae::kLinStageBlocks), plan.split) * qvae::kLinStageBlocks;
+  // two stages of weights beside the codes where two CTAs share an SM
+  const int64_t smem = linear_smem_besides_ring(E) + blocks * qvae::kLinFuseRows * qvae::kFp8Block + qvae::kLinFuseScales +
+                       2 * qvae::kLinStageBlocks * qvae::kLinATile;
   return !plan.pair && plan.NT <= qvae::kLinFuseRows && plan.max_tiles * plan.split <= (plan.split > 1 ? 2 : 1) * sms &&
-         blocks <= qvae::kLinFuseBlocks && std::min<int64_t>(M, plan.NT) * blocks <= qvae::kLinFuseItems;
+         blocks <= qvae::kLinFuseBlocks && std::min<int64_t>(M, plan.NT) * blocks <= qvae::kLinFuseItems &&
+         smem <= (plan.split > 1 ? (kSmemLimit - 1024) / 2 : kSmemLimit);
 }
 
 // The layer from bf16 rows: one launch for few rows; else the quantiser into the workspace, then the product.
