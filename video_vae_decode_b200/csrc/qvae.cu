@@ -723,6 +723,11 @@ uint32_t linear_smem_besides_ring(int64_t E) {
   return 1024u + qvae::kLinOutWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u + 4u * static_cast<uint32_t>(3 * E + 1);
 }
 
+// Shared memory of a CTA: all of it, or half where a launch of clusters with one tile each has more CTAs than SMs.
+uint32_t linear_room(const LinPlan& p, int sms) {
+  return p.split > 1 && p.max_tiles * p.split * (p.pair ? 2 : 1) > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
+}
+
 // The bf16 rows of a product that quantises them itself.
 struct LinRows {
   const void* x;
@@ -780,8 +785,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     a.stage_bytes = qvae::kLinStageBlocks * qvae::kLinATile;
   }
   const uint32_t rest = linear_smem_besides_ring(E) + (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
-  // (clusters with one tile each may sit two to an SM)
-  const uint32_t room = plan.split > 1 && plan.max_tiles * ctas > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
+  const uint32_t room = linear_room(plan, sms);
   a.stages = std::min<int>(qvae::kLinMaxStages, (room - rest) / a.stage_bytes);
   if (fuse || plan.split > 1) {  // as many as there are; a split tile's sums, NT * 512 bytes, take the ring's place
     const int sums = plan.split > 1 ? static_cast<int>(ceil_div(a.NT * qvae::kFp8Block * 4, a.stage_bytes)) : 1;
@@ -857,12 +861,12 @@ bool quantises_itself(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, 
   const LinPlan plan = known_plan(E, M, N, K, grouped, sms);
   const int64_t blocks =
       ceil_div(ceil_div(ceil_div(K, qvae::kFp8Block), qvae::kLinStageBlocks), plan.split) * qvae::kLinStageBlocks;
-  // two stages of weights beside the codes where two CTAs share an SM
+  // two stages of weights beside the codes
   const int64_t smem = linear_smem_besides_ring(E) + blocks * qvae::kLinFuseRows * qvae::kFp8Block + qvae::kLinFuseScales +
                        2 * qvae::kLinStageBlocks * qvae::kLinATile;
   return !plan.pair && plan.NT <= qvae::kLinFuseRows && plan.max_tiles * plan.split <= (plan.split > 1 ? 2 : 1) * sms &&
          blocks <= qvae::kLinFuseBlocks && std::min<int64_t>(M, plan.NT) * blocks <= qvae::kLinFuseItems &&
-         smem <= (plan.split > 1 ? (kSmemLimit - 1024) / 2 : kSmemLimit);
+         smem <= linear_room(plan, sms);
 }
 
 // The layer from bf16 rows: one launch for few rows; else the quantiser into the workspace, then the product.
