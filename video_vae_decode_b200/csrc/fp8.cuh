@@ -508,9 +508,12 @@ struct LinTiles {
 // and its commits arrive on the barriers of both.
 //
 // Split along K: where few rows leave too few tiles for the SMs, a cluster of
-// `split` CTAs (or pairs) takes one tile, each a part of its K.  The sums of each are put in its shared memory, added in the order
-// of the ranks over distributed shared memory (no atomics: the same bits every
-// time, and no workspace), and written.
+// `split` CTAs (or pairs) takes one tile, each a part of its K.  The sums of
+// each are put in its shared memory, added in the order of the ranks over
+// distributed shared memory (no atomics: the same bits every time, and no
+// workspace), and written.  (Pushing them into the adding CTA's memory with
+// asynchronous stores counted on a barrier there was no faster for one row and
+// took 12.0 us instead of 10.3 for 16 rows, 8192 x 4096.)
 //
 // kFuse (single CTAs, one tile each): the rows are bf16 and eight warps quantise
 // the CTA's part of them -- the codes, scales and outputs of the quantiser and

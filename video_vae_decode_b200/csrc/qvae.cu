@@ -631,6 +631,8 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
       const double step = pair ? std::max(64 + n / 4, n / 2) : 64 + n / 2;
       for (int split = 1; split * ctas <= qvae::kLinMaxSplit; ++split) {
         if (split > stages || (forced && g_lin_force[2] && split != std::min<int64_t>(g_lin_force[2], stages))) continue;
+        // a further CTA that leaves the longest part as it is does not pay
+        if (!(forced && g_lin_force[2]) && split > 1 && ceil_div(stages, split) == ceil_div(stages, split - 1)) continue;
         // one tile to a cluster: what the offsets give at most must fit the device (small single CTAs: twice)
         const bool twice = !pair && nt <= 32;
         if (split > 1 && max_tiles * split * ctas > (twice ? 2 : 1) * sms) continue;
