@@ -17,7 +17,7 @@
  *
  * Conventions for every entry point:
  *   - Tensor pointers are DEVICE pointers owned by the caller, 16-byte
- *     aligned.  bf16 tensors are channels_last: [N][T][H][W][C], C fastest.
+ *     aligned (unless an entry point says otherwise).  bf16 tensors are channels_last: [N][T][H][W][C], C fastest.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Calls only
  *     enqueue work; nothing synchronises the host, and scales stay on the
  *     device.  The library allocates no device memory.
@@ -48,7 +48,7 @@ extern "C" {
 typedef enum qvae_status {
   QVAE_OK = 0,
   QVAE_ERR_ARG = 1,      /* null pointer, negative size, bad workspace */
-  QVAE_ERR_SHAPE = 2,    /* Cin or Cout not a multiple of 32, or sizes out of range */
+  QVAE_ERR_SHAPE = 2,    /* sizes out of range, or a convolution's Cin or Cout not a multiple of 32 */
   QVAE_ERR_ALIGN = 3,    /* a pointer is not 16-byte aligned */
   QVAE_ERR_CUDA = 4,     /* a CUDA call or kernel launch failed */
   QVAE_ERR_TIMEOUT = 5,  /* a device-side pipeline wait ran out of time */

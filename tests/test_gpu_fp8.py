@@ -607,3 +607,49 @@ def test_few_rows_of_many_experts_and_large_layers(q, m, n, k, split):
         assert q.qvae_get_error() == 0
     finally:
         q.qvae_set_linear_tiling()
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_layers(q, seed):
+    g = torch.Generator().manual_seed(1000 + seed)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    size = lambda hi: min(hi, max(1, int(2 ** (float(torch.rand(1, generator=g)) * torch.tensor(float(hi)).log2()))))
+    m, n, k, e, pad = size(900), size(700), size(2500), r(1, 6), r(0, 9)
+    silu, bias, grouped = r(0, 1) == 1, r(0, 1) == 1, r(0, 1) == 1
+    x = rows(m, (2 if silu else 1) * k, seed, pad)
+    w, b = matrix((e, n, k), seed), matrix((e, n), seed + 1) if bias else None
+    wide = torch.full((m, n + r(0, 5)), 3.25, dtype=torch.bfloat16, device="cuda")
+    out = wide[:, :n]
+    codes, words = q.fp8_quant_act(x, silu_mul=silu)
+    byte = scale_bytes(words, -(-k // 128)).double()
+    xv = (by_row(codes).view(torch.float8_e4m3fn).double().view(m, -1, 128) * torch.exp2(byte - 127)[:, :, None]).view(m, -1)[:, :k]
+    if not silu:
+        assert torch.equal(xv, ref.act_values(x))
+    if grouped:
+        cuts = sorted(r(0, m) for _ in range(e + 1))
+        p, o = q.fp8_quantize_weights(w), torch.tensor(cuts, dtype=torch.int32, device="cuda")
+        q.linear_fp8_grouped_fused(x, o, p, b, silu_mul=silu, out=out)
+        parts = [(i, cuts[i], cuts[i + 1]) for i in range(e)]
+        assert (out[:cuts[0]] == 3.25).all() and (out[cuts[-1]:] == 3.25).all()
+    else:
+        q.linear_fp8_fused(x, q.fp8_quantize_weights(w[0]), None if b is None else b[0], silu_mul=silu, out=out)
+        parts = [(0, 0, m)]
+    assert q.qvae_get_error() == 0
+    assert (wide[:, n:] == 3.25).all()
+    for i, lo, hi in parts:
+        if hi > lo:
+            y, s = ref.linear(xv[lo:hi], ref.weight_values(w[i]), None if b is None else b[i])
+            check_product(out[lo:hi], y, s, k)
+
+
+@pytest.mark.parametrize("m,n,k", [(600000, 4096, 128), (1, 128, 1 << 20), (3, 1 << 20, 40), (1 << 20, 24, 136)])
+def test_sizes_beyond_32_bits_and_longest(q, m, n, k):
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randn((m, k), generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn((n, k), generator=gen, device="cuda") * k ** -0.5).to(torch.bfloat16)
+    out = q.linear_fp8_fused(x, q.fp8_quantize_weights(w))
+    assert q.qvae_get_error() == 0
+    wv = ref.weight_values(w)
+    for lo in sorted({0, m // 2, max(0, m - 40)}):      # the first, middle and last rows
+        y, s = ref.linear(ref.act_values(x[lo:lo + 40]), wv)
+        check_product(out[lo:lo + 40], y, s, k)

@@ -940,7 +940,7 @@ const char* qvae_status_string(int status) {
   switch (status) {
     case QVAE_OK: return "ok";
     case QVAE_ERR_ARG: return "invalid argument";
-    case QVAE_ERR_SHAPE: return "unsupported shape (Cin and Cout must be multiples of 32)";
+    case QVAE_ERR_SHAPE: return "unsupported shape (a convolution's Cin and Cout must be multiples of 32)";
     case QVAE_ERR_ALIGN: return "pointer not 16-byte aligned";
     case QVAE_ERR_CUDA: return "CUDA error";
     case QVAE_ERR_TIMEOUT: return "device-side wait timed out";
