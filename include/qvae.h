@@ -376,9 +376,9 @@ int qvae_decode_layers(const qvae_layer* layers, int32_t n, void* workspace,
  * QVAE_ERR_SHAPE otherwise.  Rows of x and out may be `ldx`, `ldo` elements apart
  * (rows of a wider buffer).  bf16 tensors (x, out, bias, w) may start at any
  * element here; rows that all start on 16 bytes are read and written faster.
- * Codes, scales and workspaces are 16-byte aligned.  out must not overlap what
- * a call reads.  Unlike the convolution, no call restricts what may be
- * launched right before it.  Needs nothing of earlier calls; calls on
+ * Codes, scales and workspaces are 16-byte aligned, offsets 4-byte.  out must
+ * not overlap what a call reads.  Unlike the convolution, no call restricts
+ * what may be launched right before it.  Needs nothing of earlier calls; calls on
  * different streams are independent as long as their buffers are.
  */
 

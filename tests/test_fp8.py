@@ -104,7 +104,7 @@ def test_product_argument_checks(E):
 
 
 def test_grouped_argument_checks():
-    assert product(E=3, offsets=None) == ARG
+    assert product(E=3, offsets=None) == ARG and product(E=3, offsets=ctypes.c_void_p(0x10002)) == ALIGN
     assert product(E=0) == SHAPE and product(E=1025) == SHAPE and product(E=-1) == ARG
 
 
@@ -133,6 +133,7 @@ def test_fused_argument_checks(E, M):
     assert fused(E=E, M=M, ldx=1 << 62) == SHAPE and fused(E=E, M=M, ldo=1 << 62) == SHAPE
     if E:
         assert fused(E=E, M=M, offsets=None) == ARG
+        assert fused(E=E, M=M, offsets=ctypes.c_void_p(0x10002)) == ALIGN
 
 
 def test_binding_refuses_tensors_that_are_not_on_a_gpu():

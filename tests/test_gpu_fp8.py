@@ -653,3 +653,29 @@ def test_sizes_beyond_32_bits_and_longest(q, m, n, k):
     for lo in sorted({0, m // 2, max(0, m - 40)}):      # the first, middle and last rows
         y, s = ref.linear(ref.act_values(x[lo:lo + 40]), wv)
         check_product(out[lo:lo + 40], y, s, k)
+
+
+FIRST_CALL = """
+import torch
+from video_vae_decode_b200 import qvae as q
+x = torch.randn(200, 512, device="cuda").to(torch.bfloat16)
+w = q.fp8_quantize_weights(torch.randn(3, 256, 512, device="cuda").to(torch.bfloat16))
+o = torch.tensor([0, 3, 100, 200], dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = q.linear_fp8_grouped_fused(x, o, w)
+    z = q.linear_fp8_grouped_fused(x[:3], torch.clamp(o, max=3), w)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, q.linear_fp8_grouped_fused(x, o, w))
+assert torch.equal(z, q.linear_fp8_grouped_fused(x[:3], torch.clamp(o, max=3), w))
+assert q.qvae_get_error() == 0
+print("ok")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture(q):
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and res.stdout.strip() == "ok", res.stderr[-2000:]

@@ -395,11 +395,11 @@ struct LinArgs {
   int NT;                // most rows of a tile (a multiple of 16)
   int spans;             // spans of a single layer's rows
   int span_group;        // spans walked under each output tile (see LinTiles)
-  int box_rows;          // rows of a CTA's part of a tile, rounded up to whole small boxes
+  int box_rows;          // most rows of a CTA's part of a tile, rounded up to a box
   int stages;
-  uint32_t stage_bytes;  // per 128-channel block of a stage: 16 KB of weights + box_rows rows of codes
+  uint32_t stage_bytes;  // of a stage's blocks: 16 KB of weights + box_rows rows of codes each
   uint32_t acc_cols, sf_col, tmem_cols;
-  int split;             // CTAs of a cluster that share a tile along K (1, or one tile to a cluster; single CTAs)
+  int split;             // CTAs or pairs of a cluster that share a tile along K (above 1: one tile to a cluster)
   const __nv_bfloat16* x;  // (quantising variant) the rows, ldx apart
   int64_t ldx;
   int vec_x;             // (quantising variant) rows of x (and their second halves) start on 16 bytes
@@ -489,17 +489,21 @@ struct LinTiles {
 // MMA cycles.  Accumulators: lane = output channel, column = row of x.
 //
 // Pipeline stages hold two 128-channel blocks: what the issuing warp does for a
-// stage besides the MMAs themselves (waits, descriptors, commits) takes about
-// 500 cycles, the four MMAs of a block 290 (64 rows) to 540 (240 rows); with a
-// stage per block the issue bound every tile (8192 x 8192 x 4096: 252 us, and
-// the same time a stage from 32 rows to 240).
+// stage besides the MMAs themselves (waits, descriptors, commits) takes some
+// hundred cycles, the four MMAs of a block 290 (16 rows) to 500 (a pair's 240).
+// Stages of one block, although more of them fit, took 16.0 us instead of 13.4
+// for 300 x 4096 x 4096 and 226 instead of 215 for 8192 x 8192 x 4096.
 //
 // Warp roles: warp 0 loads (a stage's weights as one 32 KB box that is already
 // in the MMA's order, its rows' codes as one box of the height that holds them:
-// a load takes the issuing thread about 100 cycles whatever its size, and boxes
-// of 32 rows bound ragged tiles), warp 1 owns TMEM and issues the MMAs, warps 2-5 write the scale words of each group of four
-// 128-channel blocks into TMEM (every lane quarter holds a copy: warp % 4 is
-// the quarter a warp can reach), warps 6-9 write the outputs.
+// a load takes the issuing thread about 100 cycles whatever its size), warp 1
+// owns TMEM and issues the MMAs, warps 2-5 write the scale words of each group
+// of four 128-channel blocks into TMEM (every lane quarter holds a copy: warp %
+// 4 is the quarter a warp can reach), warps 6-9 write the outputs.
+//
+// Measured, product alone: 8192 x 8192 x 4096 in 209-215 us (2.6 PFLOP/s; tensor
+// pipe 89 % active, at the power cap in a loop), 16384 rows over 64 experts of
+// 2048 x 2048 in 87 us, 64 rows over 24 of 32 such experts in 20 us (5.0 TB/s).
 //
 // kPair: a CTA pair runs the tensor cores' cta_group::2 path.  A tile is then
 // 256 output channels; each CTA loads its own 128 rows of weights and half of
@@ -518,11 +522,11 @@ struct LinTiles {
 // kFuse (single CTAs, one tile each): the rows are bf16 and eight warps quantise
 // the CTA's part of them -- the codes, scales and outputs of the quantiser and
 // the product, in one launch.  Every CTA of a row does it again, so it is for
-// few rows: one pass of the warps.  (16 rows in several passes took 8000 cycles
-// or more behind the weights' loads: 14 us for 16 x 8192 x 4096, the two
-// launches 12.)  It is done once, in front of the MMAs, while the ring fills
-// with weights: a stage at a time beside the MMAs its chain of barriers took
-// 2200 cycles a stage.
+// few rows: one pass of the warps (1 x 2048 x 2048 5.1 us, the two launches
+// 5.9; 4 x 4096 x 4096 6.8 and 7.2; with two passes, 16 x 4096 x 4096, 8.3 and
+// 7.4).  It is done once, in front of the MMAs, while the ring fills with
+// weights: a stage at a time beside the MMAs its chain of barriers took 2200
+// cycles a stage.
 //
 // Launched as a programmatic dependent.  With `early` (the quantiser of the
 // same call in front) the first weights are loaded before its end is waited

@@ -53,6 +53,7 @@ int cuda_fail(cudaError_t e, const char* what) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int current_device(int* dev) {
   QVAE_CUDA(cudaGetDevice(dev));
@@ -748,7 +749,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   if ((!rows && (!xq || !x_scale)) || !wq || !w_scale || !out || ldo < N) return QVAE_ERR_ARG;
   if (ldo > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
   if (!aligned16(xq) || !aligned16(x_scale) || !aligned16(wq) || !aligned16(w_scale) || !aligned2(bias) ||
-      !aligned2(out))
+      !aligned2(out) || !aligned4(offsets))
     return QVAE_ERR_ALIGN;
   const bool fuse = rows != nullptr;
   int dev, sms;
@@ -883,7 +884,8 @@ int launch_linear_fused(int64_t E, int64_t M, int64_t N, int64_t K, int op, cons
   if (!wq || !w_scale || !out || ldo < N || !workspace || workspace_bytes < qvae_fp8_workspace_bytes(M, K))
     return QVAE_ERR_ARG;
   if (ldo > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
-  if (!aligned16(wq) || !aligned16(w_scale) || !aligned2(bias) || !aligned2(out) || !aligned16(workspace))
+  if (!aligned16(wq) || !aligned16(w_scale) || !aligned2(bias) || !aligned2(out) || !aligned4(offsets) ||
+      !aligned16(workspace))
     return QVAE_ERR_ALIGN;
   const LinRows rows = {x, ldx, op == QVAE_FP8_SILU_MUL};
   if (!x || ldx < (rows.silu ? 2 * K : K)) return QVAE_ERR_ARG;
