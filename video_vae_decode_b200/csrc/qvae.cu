@@ -605,10 +605,10 @@ int64_t linear_tiles(int64_t E, int64_t M, int64_t nblk, bool grouped, bool pair
 // The tiling with the least estimated time, in SM cycles.  A 32-channel step of a tile costs what shared memory moves
 // for it at 128 bytes a cycle -- 4 KB of weights in and out, n rows of 32 codes in and out (a pair: half of them to a
 // CTA) -- or the tensor cores' n / 2 cycles, whichever is longer (measured: 78 cycles at n = 16, 114 at 128, pairs 120 at
-// 240).  What a launch takes besides was measured on
-// small shapes: about 6000 cycles until the first MMA, an epilogue of 11 cycles a row (22 where half of the warps write
-// it beside the next tile), and for a split along K the sums'
-// way over distributed shared memory.  Weights come at 3300 bytes a cycle at most, and 30 to an SM.
+// 240).  What a launch takes besides was measured on small shapes: about 6000 cycles until the first MMA, an epilogue of
+// 11 cycles a row (22 where half of the warps write it beside the next tile), and for a split along K the larger
+// cluster's start and the sums' way over distributed shared memory (1 x 2048 x 2048: split 2 5.7 us, 4 5.0, 8 5.8).
+// Weights come at 3300 bytes a cycle at most, and 30 to an SM.
 LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms, bool forced = true) {
   const int64_t nblk = ceil_div(N, qvae::kFp8Block), Kb = ceil_div(K, qvae::kFp8Block);
   const int64_t stages = ceil_div(Kb, qvae::kLinStageBlocks);
@@ -644,8 +644,9 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
         const double reading = std::min<double>(sms, tiles * split * ctas);         // SMs
         const double epilogue = 1300 + (waves > 1 ? 22 : 11) * n;
         const double steps = waves * part * shared, bytes = weights / std::min(3300.0, 30 * reading);
+        const double joining = split > 1 ? 1700 + 500 * split + 15 * n : 0;
         const double time = 6000 + std::max(steps, bytes) + 0.25 * std::min(steps, bytes) +
-                            (waves - 1) * std::max(0.0, epilogue - part) + epilogue + (split > 1 ? 2700 + 200 * split + 15 * n : 0) + (pair ? 1500 : 0);
+                            (waves - 1) * std::max(0.0, epilogue - part) + epilogue + joining + (pair ? 1500 : 0);
         if (!best.NT || time < least) {
           best = {pair, nt, split, max_tiles};
           least = time;
