@@ -739,8 +739,8 @@ struct LinRows {
   bool silu;
 };
 
-// offsets null: one span of M rows.  rows: quantised by the product (xq and x_scale unused).  early: the kernel before this one on the stream is the quantiser, which lets this
-// one start only when all that came before it has finished.
+// offsets null: one span of M rows.  rows: quantised by the product (xq and x_scale unused).  early: the kernel before
+// this one on the stream is the quantiser, which lets this one start only when all that came before it has finished.
 int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq, const uint32_t* x_scale,
                   const int32_t* offsets, const uint8_t* wq, const uint8_t* w_scale, const void* bias, void* out,
                   int64_t ldo, cudaStream_t stream, bool early = false, const LinRows* rows = nullptr) {

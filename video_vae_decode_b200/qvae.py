@@ -489,9 +489,12 @@ def _buffer(t: torch.Tensor, dtype: torch.dtype, count: int, device: int, name: 
     return t.data_ptr()
 
 
+_bf16 = torch.bfloat16
+
+
 def _rows(t: torch.Tensor, columns: int, device: int, name: str):
     """(rows, elements between them) of a bf16 matrix whose columns are adjacent."""
-    if t.get_device() != device or t.dtype is not torch.bfloat16 or t.dim() != 2:
+    if t.get_device() != device or t.dtype is not _bf16 or t.dim() != 2:
         raise ValueError(f"{name}: a bf16 matrix on cuda:{device} is needed")
     m, n = t.shape
     ld, step = t.stride()
@@ -528,10 +531,13 @@ def _elsewhere(device: int, stream):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
+# (a CUDA tensor is at hand: torch has initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _run(device: int, stream, call, *args):
     """call(handle, *args) on `device` and `stream` (None: the device's current stream)."""
-    if stream is None and device == torch.cuda.current_device():
+    if stream is None and device == _current_device():
         return call(_raw_stream(device), *args)
     with _elsewhere(device, stream) as handle:
         return call(handle, *args)
@@ -580,8 +586,8 @@ def fp8_quant_act(x: torch.Tensor, silu_mul: bool = False, stream=None):
     return _run(device, stream, call)
 
 
-def _layer(weights: Fp8Weights, M: int, bias, out, offsets):
-    """Checks what every product takes; (row stride of out, addresses of bias and offsets)."""
+def _extras(weights: Fp8Weights, bias, offsets):
+    """Addresses of the bias and the offsets (None: none), checked."""
     E, N, device = weights.E, weights.N, weights.device
     po = pb = None
     if offsets is not None:
@@ -592,23 +598,33 @@ def _layer(weights: Fp8Weights, M: int, bias, out, offsets):
         if tuple(bias.shape) != (E, N) and (E != 1 or tuple(bias.shape) != (N,)):
             raise ValueError(f"bias: [N] or [E, N] is needed, N = {N}, E = {E}")
         pb = _buffer(bias, torch.bfloat16, E * N, device, "bias")
+    return pb, po
+
+
+def _out(out, M: int, N: int, device: int):
+    """(out, elements between its rows); a new one for None."""
     if out is None:
-        return N, pb, po
+        return torch.empty((M, N), dtype=torch.bfloat16, device=torch.device("cuda", device)), N
     rows, ldo = _rows(out, N, device, "out")
     if rows != M:
         raise ValueError(f"out: {M} rows are needed")
-    return ldo, pb, po
+    return out, ldo
 
 
-def _product_call(handle, name, xq, x_scale, weights, out, ldo, pb, po):
-    M, N = xq.shape[1], weights.N
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+def _product(handle, name, xq, x_scale, weights, bias, out, offsets):
+    N, K, device = weights.N, weights.K, weights.device
+    if xq.dim() != 3 or xq.shape[0] != -(-K // 128) or xq.shape[2] != 128:
+        raise ValueError(f"xq: codes [{-(-K // 128)}, rows, 128] of {K} input channels are needed")
+    M = xq.shape[1]
+    _buffer(xq, torch.uint8, xq.numel(), device, "xq")
+    _buffer(x_scale, torch.int32, M * -(-K // 512), device, "x_scale")
+    pb, po = _extras(weights, bias, offsets)
+    out, ldo = _out(out, M, N, device)
     if po is None:
-        status = lib().qvae_linear_fp8(M, N, weights.K, xq.data_ptr(), x_scale.data_ptr(), weights.wq.data_ptr(),
+        status = lib().qvae_linear_fp8(M, N, K, xq.data_ptr(), x_scale.data_ptr(), weights.wq.data_ptr(),
                                        weights.w_scale.data_ptr(), pb, out.data_ptr(), ldo, handle)
     else:
-        status = lib().qvae_linear_fp8_grouped(weights.E, M, N, weights.K, xq.data_ptr(), x_scale.data_ptr(), po,
+        status = lib().qvae_linear_fp8_grouped(weights.E, M, N, K, xq.data_ptr(), x_scale.data_ptr(), po,
                                                weights.wq.data_ptr(), weights.w_scale.data_ptr(), pb, out.data_ptr(),
                                                ldo, handle)
     if status:
@@ -616,21 +632,10 @@ def _product_call(handle, name, xq, x_scale, weights, out, ldo, pb, po):
     return out
 
 
-def _product(name, xq, x_scale, weights, bias, out, offsets, stream):
-    K, device = weights.K, weights.device
-    if xq.dim() != 3 or xq.shape[0] != -(-K // 128) or xq.shape[2] != 128:
-        raise ValueError(f"xq: codes [{-(-K // 128)}, rows, 128] of {K} input channels are needed")
-    M = xq.shape[1]
-    _buffer(xq, torch.uint8, xq.numel(), device, "xq")
-    _buffer(x_scale, torch.int32, M * -(-K // 512), device, "x_scale")
-    ldo, pb, po = _layer(weights, M, bias, out, offsets)
-    return _run(device, stream, _product_call, name, xq, x_scale, weights, out, ldo, pb, po)
-
-
 def linear_fp8(xq: torch.Tensor, x_scale: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """bf16 [M, N] of quantised rows (fp8_quant_act) and one weight matrix."""
-    return _product("qvae_linear_fp8", xq, x_scale, weights, bias, out, None, stream)
+    return _run(weights.device, stream, _product, "qvae_linear_fp8", xq, x_scale, weights, bias, out, None)
 
 
 def linear_fp8_grouped(xq: torch.Tensor, x_scale: torch.Tensor, offsets: torch.Tensor, weights: Fp8Weights,
@@ -640,16 +645,19 @@ def linear_fp8_grouped(xq: torch.Tensor, x_scale: torch.Tensor, offsets: torch.T
     expert e's matrix; other rows of out are left as they are."""
     if offsets is None:
         raise ValueError("offsets: an int32 tensor is needed")
-    return _product("qvae_linear_fp8_grouped", xq, x_scale, weights, bias, out, offsets, stream)
+    return _run(weights.device, stream, _product, "qvae_linear_fp8_grouped", xq, x_scale, weights, bias, out, offsets)
 
 
-def _fused_call(handle, name, x, M, ldx, weights, op, out, ldo, workspace, pb, po):
+def _fused(handle, name, x, weights, bias, silu_mul, out, workspace, offsets):
     N, K, device = weights.N, weights.K, weights.device
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    M, ldx = _rows(x, 2 * K if silu_mul else K, device, "x")
+    # (for one layer without a bias there is nothing to look at: a small layer's time is the host's)
+    pb, po = (None, None) if bias is None and offsets is None and weights.E == 1 else _extras(weights, bias, offsets)
+    out, ldo = _out(out, M, N, device)
     if workspace is None:
         workspace = fp8_workspace(M, K, x.device)
     pk = _buffer(workspace, torch.uint8, 0, device, "workspace")
+    op = QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN
     if po is None:
         status = lib().qvae_linear_fp8_fused(M, N, K, op, x.data_ptr(), ldx, weights.wq.data_ptr(),
                                              weights.w_scale.data_ptr(), pb, out.data_ptr(), ldo, pk, workspace.numel(),
@@ -663,19 +671,12 @@ def _fused_call(handle, name, x, M, ldx, weights, op, out, ldo, workspace, pb, p
     return out
 
 
-def _fused(name, x, weights, bias, silu_mul, out, workspace, offsets, stream):
-    device = weights.device
-    M, ldx = _rows(x, 2 * weights.K if silu_mul else weights.K, device, "x")
-    ldo, pb, po = _layer(weights, M, bias, out, offsets)
-    return _run(device, stream, _fused_call, name, x, M, ldx, weights, QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN,
-                out, ldo, workspace, pb, po)
-
-
 def linear_fp8_fused(x: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None, silu_mul: bool = False,
                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
     """bf16 [M, N] of bf16 rows x [M, K] (silu_mul: [M, 2 K] = [gate | up]), quantised on the way."""
-    return _fused("qvae_linear_fp8_fused", x, weights, bias, silu_mul, out, workspace, None, stream)
+    return _run(weights.device, stream, _fused, "qvae_linear_fp8_fused", x, weights, bias, silu_mul, out, workspace,
+                None)
 
 
 def linear_fp8_grouped_fused(x: torch.Tensor, offsets: torch.Tensor, weights: Fp8Weights,
@@ -685,7 +686,8 @@ def linear_fp8_grouped_fused(x: torch.Tensor, offsets: torch.Tensor, weights: Fp
     """linear_fp8_grouped of bf16 rows, quantised on the way."""
     if offsets is None:
         raise ValueError("offsets: an int32 tensor is needed")
-    return _fused("qvae_linear_fp8_grouped_fused", x, weights, bias, silu_mul, out, workspace, offsets, stream)
+    return _run(weights.device, stream, _fused, "qvae_linear_fp8_grouped_fused", x, weights, bias, silu_mul, out,
+                workspace, offsets)
 
 
 # ---------------------------------------------------------------- control
