@@ -651,7 +651,7 @@ def linear_fp8_grouped(xq: torch.Tensor, x_scale: torch.Tensor, offsets: torch.T
 def _fused(handle, name, x, weights, bias, silu_mul, out, workspace, offsets):
     N, K, device = weights.N, weights.K, weights.device
     M, ldx = _rows(x, 2 * K if silu_mul else K, device, "x")
-    # (for one layer without a bias there is nothing to look at: a small layer's time is the host's)
+    # (one layer without a bias has nothing to check there: a small layer's time is the host's, 6.5 us a call here)
     pb, po = (None, None) if bias is None and offsets is None and weights.E == 1 else _extras(weights, bias, offsets)
     out, ldo = _out(out, M, N, device)
     if workspace is None:
