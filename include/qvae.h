@@ -377,9 +377,10 @@ int qvae_decode_layers(const qvae_layer* layers, int32_t n, void* workspace,
  * (rows of a wider buffer).  bf16 tensors (x, out, bias, w) may start at any
  * element here; rows that all start on 16 bytes are read and written faster.
  * Codes, scales and workspaces are 16-byte aligned, offsets 4-byte.  out must
- * not overlap what a call reads.  Unlike the convolution, no call restricts
- * what may be launched right before it.  Needs nothing of earlier calls; calls on
- * different streams are independent as long as their buffers are.
+ * not overlap what a call reads (out == x is refused).  Unlike the convolution,
+ * no call restricts what may be launched right before it.  Needs nothing of
+ * earlier calls; calls on different streams are independent as long as their
+ * buffers are.
  */
 
 /* What a layer quantises of its bf16 rows. */

@@ -131,6 +131,7 @@ def test_fused_argument_checks(E, M):
     assert fused(E=E, M=M, op=3) == ARG and fused(E=E, M=M, ldx=127) == ARG and fused(E=E, M=M, op=1, ldx=255) == ARG
     assert fused(E=E, M=M, ldo=127) == ARG and fused(E=E, M=M, N=0) == SHAPE and fused(E=E, M=-M) == ARG
     assert fused(E=E, M=M, ldx=1 << 62) == SHAPE and fused(E=E, M=M, ldo=1 << 62) == SHAPE
+    assert fused(E=E, M=M) == ARG and fused(E=E, M=M, op=1, ldo=256) == ARG  # in place
     if E:
         assert fused(E=E, M=M, offsets=None) == ARG
         assert fused(E=E, M=M, offsets=ctypes.c_void_p(0x10002)) == ALIGN

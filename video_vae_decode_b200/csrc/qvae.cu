@@ -892,6 +892,7 @@ int launch_linear_fused(int64_t E, int64_t M, int64_t N, int64_t K, int op, cons
   if (!x || ldx < (rows.silu ? 2 * K : K)) return QVAE_ERR_ARG;
   if (ldx > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
   if (!aligned2(x)) return QVAE_ERR_ALIGN;
+  if (x == out) return QVAE_ERR_ARG;  // in one launch a CTA's outputs would meet rows that others still read
   int dev, sms;
   if ((rc = current_device(&dev))) return rc;
   if ((rc = sm_count(dev, &sms))) return rc;
