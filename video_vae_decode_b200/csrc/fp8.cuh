@@ -1125,12 +1125,16 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
       add(IntC<8>{});
     }
     // no CTA leaves while another may still read its sums: waited for at the very end
+    tc_fence_before();
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    cluster_arrive();
   }
   tc_fence_before();
   if (kPair) {
-    cluster_sync();  // neither CTA leaves while its partner may still touch its memory
+    // neither CTA leaves, or frees the pair's TMEM, while its partner may still touch its memory.  (A split pair has
+    // arrived above, with its last reads of TMEM behind it: this wait is that arrive's, and the end's.)
+    if (!split) cluster_arrive();
+    cluster_wait();
   } else {
     __syncthreads();
   }
@@ -1143,9 +1147,9 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
       tmem_dealloc(tmem_base, a.tmem_cols);
     }
   }
-  if (split) {
+  if (split && !kPair) {
     __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_wait();
   }
 }
 

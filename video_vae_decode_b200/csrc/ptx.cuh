@@ -282,10 +282,17 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t local, uint32_t rank) {
   return r;
 }
 
-// All threads of every CTA in the cluster.
-__device__ __forceinline__ void cluster_sync() {
+// All threads of every CTA in the cluster.  A cluster has one such barrier, with one phase at a time: every arrive is
+// followed by its wait before the thread arrives again.
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 
 // Arrive on a barrier of another CTA of the cluster.
