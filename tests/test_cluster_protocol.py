@@ -99,3 +99,24 @@ def test_the_reader_of_the_source_sees_two_arrives():
     assert operations(text, {"split": True, "kPair": False}) == ["A", "W", "A", "W"]
     with pytest.raises(AssertionError):
         operations("if (warp == 1) { cluster_sync(); }", {"split": True})
+
+
+def test_signals_between_the_ctas_of_a_linear_pair_are_at_cluster_scope():
+    # barriers that the partner's threads arrive on: scale words in place, accumulator read
+    text, ptx = body(source("fp8.cuh"), "linear_fp8_kernel"), source("ptx.cuh")
+    assert "mbar_arrive_remote" not in text                              # (CTA scope)
+    arrive = body(ptx, "void mbar_arrive_cluster_relaxed")
+    assert "mbarrier.arrive.relaxed.cluster.shared::cluster" in arrive
+    assert "mbarrier.try_wait.parity.relaxed.cluster" in body(ptx, "bool mbar_try_wait_cluster_relaxed")
+    signalled = re.findall(r"mbar_arrive_cluster_relaxed\((?:map_to_cta\()?(\w+)", text)
+    assert sorted(signalled) == ["empty_leader", "sf_full"]
+    assert re.search(r"empty_leader = kPair \? map_to_cta\(acc_empty, lead_cta\)", text)
+    waits = re.findall(r"(\w+)\((sf_full|acc_empty) \+", text)
+    waits = [w for w in waits if w[0] != "mbar_init" and w[0] != "map_to_cta" and w[0] != "mbar_arrive"]
+    assert sorted(waits) == [("wait_tmem", "acc_empty"), ("wait_tmem", "sf_full")]
+    assert "mbar_wait_warp<kPair>" in text[text.index("auto wait_tmem"):text.index("auto commit")]
+    # each stands behind its fence, and the waits in front of theirs
+    for name in ("sf_full", "empty_leader"):
+        at = text.index("mbar_arrive_cluster_relaxed(" + ("map_to_cta(" if name == "sf_full" else "") + name)
+        assert "tc_fence_before();" in text[at - 300:at], name
+    assert "tc_fence_after();" in text[text.index("wait_tmem(sf_full"):][:250]

@@ -313,12 +313,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
 // A whole warp's wait for a phase.  Mostly the phase is there, or comes within
 // the time that one try waits by itself: the warp then goes on without
 // diverging (one lane waiting and telling the others cost about 280 cycles
-// each time).  Else lane 0 waits within the time limit.
+// each time).  Else lane 0 waits within the time limit.  kTmem: a signal from either CTA of a pair behind which only
+// TMEM is touched (see mbar_try_wait_cluster_relaxed).
+template <bool kTmem = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns,
                                                int err_code) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xFFFFFFFFu, kTmem ? mbar_try_wait_cluster_relaxed(bar, parity) : mbar_try_wait(bar, parity))) return true;
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, limit_ns, err_code);
+  if ((threadIdx.x & 31) == 0)
+    ok = kTmem ? mbar_wait_cluster<true>(bar, parity, abort_flag, limit_ns, err_code)
+               : mbar_wait(bar, parity, abort_flag, limit_ns, err_code);
   ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
   __syncwarp();
   return ok != 0;
@@ -808,6 +812,10 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return mbar_wait_warp(bar, parity, abort_flag, limit, kErrTimeoutMma);
     };
+    // scale words written, accumulator read: signals from both CTAs of a pair (kFuse: with the codes in shared memory)
+    auto wait_tmem = [&](uint32_t bar, uint32_t parity) {
+      return mbar_wait_warp<kPair>(bar, parity, abort_flag, limit, kErrTimeoutMma);
+    };
     auto commit = [&](uint32_t bar) {
       if (kPair) {
         mma_commit_pair_multicast(bar, static_cast<uint16_t>(0x3u << lead_cta));
@@ -825,7 +833,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
     for (int tile = first_tile; tile < total && ok; tile += tile_step) {
       const LinTile t = tiles.at(tile);
       const uint32_t d = tmem_base + c * a.acc_cols;
-      if (!check_bounds(static_cast<uint32_t>(t.n) <= a.acc_cols) || !(ok = wait(acc_empty + 8 * c, cp ^ 1))) {
+      if (!check_bounds(static_cast<uint32_t>(t.n) <= a.acc_cols) || !(ok = wait_tmem(acc_empty + 8 * c, cp ^ 1))) {
         ok = false;
         break;
       }
@@ -836,7 +844,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
         // a scale word serves two stages (kFuse: all are there, and stay, from the first on)
         const bool last = kb + kLinStageBlocks >= kb1, first_half = (kb & 3) == 0;
         const bool group_end = !kFuse && (!first_half || last);
-        if ((kb == kb0 || (!kFuse && first_half)) && !(ok = wait(sf_full + 8 * g, gp))) break;
+        if ((kb == kb0 || (!kFuse && first_half)) && !(ok = wait_tmem(sf_full + 8 * g, gp))) break;
         if (!(ok = wait(full + 8 * s, p))) break;
         tc_fence_after();
         const uint64_t ad = ad0 + s * stage16;
@@ -929,11 +937,11 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          // what the issuer's MMAs read of this are TMEM stores that tcgen05.wait::st has seen complete: no release at
-          // cluster scope, which also waits for the next words' loads and for everything else this warp has in
-          // flight (it cost 15 % of the whole product: 237 against 205 us at 8192 x 8192 x 4096)
+          // what the issuer's MMAs read of this are TMEM stores that tcgen05.wait::st has seen complete and the fence
+          // orders: no release at cluster scope, which also waits for the next words' loads and for everything else
+          // this warp has in flight (it cost 15 % of the whole product: 237 against 205 us at 8192 x 8192 x 4096)
           if (kPair) {
-            mbar_arrive_remote(map_to_cta(sf_full + 8 * g, lead_cta));
+            mbar_arrive_cluster_relaxed(map_to_cta(sf_full + 8 * g, lead_cta));
           } else {
             mbar_arrive(sf_full + 8 * g);
           }
@@ -1049,7 +1057,7 @@ __global__ void __launch_bounds__(kLinThreads, kPair ? 1 : 2)
       __syncwarp();
       if (lane == 0) {
         if (kPair) {
-          mbar_arrive_remote(empty_leader + 8 * c);
+          mbar_arrive_cluster_relaxed(empty_leader + 8 * c);
         } else {
           mbar_arrive(acc_empty + 8 * c);
         }

@@ -73,6 +73,21 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
+// try_wait without an acquire, at cluster scope: for a barrier that threads of the other CTA of a pair arrive on
+// (mbar_arrive_cluster_relaxed) and behind which only TMEM is touched -- the tcgen05 fences on both sides of a
+// signal order that, for whatever threads the signal connects, and these are the cluster's.
+__device__ __forceinline__ bool mbar_try_wait_cluster_relaxed(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Non-blocking probe of a phase (acquire semantics when it reports completion).
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -137,13 +152,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// mbar_wait with cluster-scope acquire (see mbar_try_wait_cluster).
+// mbar_wait with cluster-scope acquire (see mbar_try_wait_cluster), or at cluster scope without one.
+template <bool kRelaxed = false>
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                   uint64_t limit_ns, int err_code) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+  auto try_wait = [&] {
+    return kRelaxed ? mbar_try_wait_cluster_relaxed(bar, parity) : mbar_try_wait_cluster(bar, parity);
+  };
+  if (try_wait()) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (try_wait()) return true;
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
       *abort_flag = 1;
@@ -299,6 +318,13 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
+}
+
+// The same without a release: behind tcgen05.wait::st or ::ld and tcgen05.fence::before_thread_sync, which order what
+// this thread did to TMEM before the signal.  A release at cluster scope would also wait for everything else that the
+// thread has in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Arrive on a barrier of another CTA of the cluster with release at CTA
