@@ -537,6 +537,11 @@ int qvae_set_linear_tiling(int32_t NT, int32_t mode, int32_t split, int32_t max_
  * split.  E = 0: a single layer; else grouped by E experts. */
 int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* out3);
 
+/* What a CTA of that product takes: out[0] = bytes of shared memory, out[1] =
+ * TMEM columns, out[2] = CTAs of its cluster.  fused != 0: of the _fused entry
+ * points' product. */
+int qvae_get_linear_footprint(int32_t E, int64_t M, int32_t N, int32_t K, int32_t fused, int32_t* out3);
+
 /*
  * How qvae_decode_layers runs quantised layers (process-wide, tuning and
  * tests): 0 (default) the quantise pass writes codes that the convolution

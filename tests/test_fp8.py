@@ -161,3 +161,49 @@ def test_binding_checks_of_layouts():
         qvae._buffer(torch.zeros(3, dtype=torch.int64), torch.int32, 3, cpu, "offsets")
     with pytest.raises(ValueError):
         qvae._buffer(torch.zeros(3, dtype=torch.int32), torch.int32, 4, cpu, "offsets")
+
+
+def test_footprint_argument_checks():
+    out = (ctypes.c_int32 * 3)()
+    L = qvae.lib()
+    assert L.qvae_get_linear_footprint(0, 4, 128, 128, 1, None) == ARG
+    assert L.qvae_get_linear_footprint(-1, 4, 128, 128, 1, out) == ARG
+    assert L.qvae_get_linear_footprint(0, 4, 0, 128, 1, out) == SHAPE
+    assert L.qvae_get_linear_footprint(0, 4, 128, 128, 1, out) == OK
+
+
+def footprints():
+    """What the CTAs of products take, automatic and forced tilings, single and grouped."""
+    sizes = [(m, n, k) for m in (1, 3, 16, 60, 100, 230, 480, 700, 5000) for n in (64, 300, 2048)
+             for k in (100, 600, 1500, 4096, 16384)]
+    tilings = [(0, 0, 0)] + [(nt, mode, split) for mode in (1, 2) for nt in (16, 32, 48, 112, 128, 224, 240)
+                             for split in (1, 2, 3, 4, 8)]
+    seen = {}
+    try:
+        for t in tilings:
+            qvae.qvae_set_linear_tiling(*t)
+            for m, n, k in sizes:
+                for e in (0, 6, 1024):
+                    for fused in (False, True):
+                        f = qvae.qvae_get_linear_footprint(e, m, n, k, fused)
+                        seen.setdefault((f["smem"], f["tmem_cols"], f["cluster"]), (t, m, n, k, e, fused))
+    finally:
+        qvae.qvae_set_linear_tiling()
+    return seen
+
+
+def test_clusters_that_can_share_an_sm_fit_its_tensor_memory():
+    # Clusters wait for one another's CTAs, and a CTA for its TMEM: two clusters that each hold columns on one SM and
+    # wait for them on another would wait for ever.  An SM has 228 KB of shared memory (1 KB of each CTA is the
+    # system's) and 512 columns.
+    seen = footprints()
+    clusters = [f for f in seen if f[2] > 1]
+    assert len(clusters) > 20 and any(f[1] == 512 for f in clusters)
+    room = 228 * 1024
+    assert min(f[0] for f in clusters) + 1024 > room / 3                 # never three on an SM
+    for a in clusters:
+        for b in clusters:
+            if a[0] + b[0] + 2 * 1024 <= room:
+                assert a[1] + b[1] <= 512, (a, seen[a], b, seen[b])
+    for f in seen:
+        assert f[0] <= 232448 and f[1] in (32, 64, 128, 256, 512), (f, seen[f])

@@ -732,6 +732,40 @@ uint32_t linear_room(const LinPlan& p, int sms) {
   return p.split > 1 && p.max_tiles * p.split * (p.pair ? 2 : 1) > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
 }
 
+// Shared memory and TMEM of a product's CTAs (a.E, Kb and NT are set).
+//
+// Clusters wait for one another's CTAs, and a CTA for its TMEM, without a time limit: no two CTAs of clusters that can
+// share an SM may want more than its 512 columns.  A split CTA of up to 256 columns takes a third of the shared memory
+// (of a pair: more than half), so that two fit and three do not; one of more columns (a split pair of 240 rows) takes
+// so much that no other fits beside it, as pairs without a split and the convolution's pairs do by themselves (170 KB
+// or more wherever they take 512 columns).
+int size_linear(qvae::LinArgs& a, const LinPlan& plan, bool fuse, int sms, uint32_t* smem) {
+  const bool split = plan.split > 1;
+  a.box_rows = (a.NT / (plan.pair ? 2 : 1) + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
+  a.stage_bytes = qvae::kLinStageBlocks * (qvae::kLinATile + (fuse ? 0u : static_cast<uint32_t>(a.box_rows) * 128u));
+  const int blocks = static_cast<int>(ceil_div(ceil_div(a.Kb, qvae::kLinStageBlocks), plan.split)) * qvae::kLinStageBlocks;
+  a.codes_bytes = fuse ? static_cast<uint32_t>(blocks) * qvae::kLinFuseRows * qvae::kFp8Block : 0u;
+  const uint32_t rest = linear_smem_besides_ring(a.E) + (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
+  a.stages = std::min<int>(qvae::kLinMaxStages, (linear_room(plan, sms) - rest) / a.stage_bytes);
+  if (fuse || split) {  // as many as there are; a split tile's sums, NT * 512 bytes, take the ring's place
+    const int sums = split ? static_cast<int>(ceil_div(a.NT * qvae::kFp8Block * 4, a.stage_bytes)) : 1;
+    a.stages = std::min(a.stages, std::max(blocks / qvae::kLinStageBlocks, sums));
+  }
+  const uint32_t ring = a.stages * a.stage_bytes;
+  if (a.stages < 1 || (split && ring < a.NT * qvae::kFp8Block * 4u)) return QVAE_ERR_UNSUPPORTED;
+  // two accumulators (a split CTA has one tile: one), read 32 columns at a time, and two sets of scale words
+  const uint32_t sf_cols = plan.pair ? qvae::kLinSfCols<true> : qvae::kLinSfCols<false>;
+  a.acc_cols = static_cast<uint32_t>(a.NT);
+  a.sf_col = (split ? 1 : 2) * a.acc_cols;
+  const uint32_t sf_sets = fuse ? static_cast<uint32_t>(blocks + 3) / 4 + 1 : 2u;  // (a part of K may start inside a group)
+  const uint32_t cols = std::max(a.sf_col + sf_sets * sf_cols, a.sf_col - a.acc_cols + (a.acc_cols + 31) / 32 * 32);
+  a.tmem_cols = 32;
+  while (a.tmem_cols < cols) a.tmem_cols <<= 1;
+  const uint32_t least = !split ? 0u : (a.tmem_cols > 256 ? 170u : plan.pair ? 116u : 78u) * 1024;
+  *smem = std::max(rest + ring, least);
+  return QVAE_OK;
+}
+
 // The bf16 rows of a product that quantises them itself.
 struct LinRows {
   const void* x;
@@ -777,40 +811,14 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.split = plan.split;
   a.early = early ? 1 : 0;
   a.tiles_n = plan.pair ? (a.nblk + 1) / 2 : a.nblk;
-  a.box_rows = (a.NT / (plan.pair ? 2 : 1) + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
-  a.stage_bytes = qvae::kLinStageBlocks * (qvae::kLinATile + static_cast<uint32_t>(a.box_rows) * 128u);
-  const int blocks = static_cast<int>(ceil_div(ceil_div(a.Kb, qvae::kLinStageBlocks), plan.split)) * qvae::kLinStageBlocks;
+  uint32_t smem;
+  if ((rc = size_linear(a, plan, fuse, sms, &smem))) return rc;
   if (fuse) {
     a.x = static_cast<const __nv_bfloat16*>(rows->x);
     a.ldx = rows->ldx;
     a.silu = rows->silu ? 1 : 0;
     a.vec_x = aligned16(rows->x) && (rows->ldx % 8 == 0 || M == 1) && (!rows->silu || K % 8 == 0);
-    a.codes_bytes = static_cast<uint32_t>(blocks) * qvae::kLinFuseRows * qvae::kFp8Block;
-    a.stage_bytes = qvae::kLinStageBlocks * qvae::kLinATile;
   }
-  const uint32_t rest = linear_smem_besides_ring(E) + (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
-  const uint32_t room = linear_room(plan, sms);
-  a.stages = std::min<int>(qvae::kLinMaxStages, (room - rest) / a.stage_bytes);
-  if (fuse || plan.split > 1) {  // as many as there are; a split tile's sums, NT * 512 bytes, take the ring's place
-    const int sums = plan.split > 1 ? static_cast<int>(ceil_div(a.NT * qvae::kFp8Block * 4, a.stage_bytes)) : 1;
-    a.stages = std::min(a.stages, std::max(blocks / qvae::kLinStageBlocks, sums));
-  }
-  const uint32_t ring = a.stages * a.stage_bytes;
-  if (a.stages < 1 || (plan.split > 1 && ring < a.NT * qvae::kFp8Block * 4u)) return QVAE_ERR_UNSUPPORTED;
-  // Clusters wait for one another's CTAs, and a CTA for its TMEM: no two CTAs that can share an SM may want more than
-  // its 512 columns.  A split CTA takes at most 256 and a third of the shared memory, so that two fit and three do not,
-  // and none fits beside a CTA that takes more columns (those take 170 KB or more).
-  // (Split pairs take more than half of the shared memory.)
-  const uint32_t least = plan.split > 1 ? (plan.pair ? 116u : 78u) * 1024 : 0u;
-  const uint32_t smem = std::max(rest + ring, least);
-  // two accumulators (a split CTA has one tile: one), read 32 columns at a time, and two sets of scale words
-  const uint32_t sf_cols = plan.pair ? qvae::kLinSfCols<true> : qvae::kLinSfCols<false>;
-  a.acc_cols = static_cast<uint32_t>(a.NT);
-  a.sf_col = (plan.split > 1 ? 1 : 2) * a.acc_cols;
-  const uint32_t sf_sets = fuse ? static_cast<uint32_t>(blocks + 3) / 4 + 1 : 2u;  // (a part of K may start inside a group)
-  const uint32_t cols = std::max(a.sf_col + sf_sets * sf_cols, a.sf_col - a.acc_cols + (a.acc_cols + 31) / 32 * 32);
-  a.tmem_cols = 32;
-  while (a.tmem_cols < cols) a.tmem_cols <<= 1;
   a.vec_out = aligned16(out) && (ldo % 8 == 0 || M == 1);
   a.offsets = offsets;
   a.x_scale = x_scale;
@@ -871,6 +879,14 @@ bool quantises_itself(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, 
   return !plan.pair && plan.NT <= qvae::kLinFuseRows && plan.max_tiles * plan.split <= (plan.split > 1 ? 2 : 1) * sms &&
          blocks <= qvae::kLinFuseBlocks && std::min<int64_t>(M, plan.NT) * blocks <= qvae::kLinFuseItems &&
          smem <= linear_room(plan, sms);
+}
+
+// SMs of the current device, or a B200's where there is none.
+int planning_sms() {
+  int sms = 148, dev;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) sm_count(dev, &sms);
+  cudaGetLastError();
+  return sms;
 }
 
 // The layer from bf16 rows: one launch for few rows; else the quantiser into the workspace, then the product.
@@ -1418,13 +1434,29 @@ int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* 
   const int rc = check_linear(std::max(E, 1), M, N, K);
   if (rc) return rc;
   if (E < 0) return QVAE_ERR_ARG;
-  int sms = 148, dev;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) sm_count(dev, &sms);
-  cudaGetLastError();
-  const LinPlan plan = plan_linear(std::max(E, 1), std::max<int64_t>(M, 1), N, K, E > 0, sms);
+  const LinPlan plan = plan_linear(std::max(E, 1), std::max<int64_t>(M, 1), N, K, E > 0, planning_sms());
   out3[0] = plan.NT;
   out3[1] = plan.pair ? 2 : 1;
   out3[2] = plan.split;
+  return QVAE_OK;
+}
+
+int qvae_get_linear_footprint(int32_t E, int64_t M, int32_t N, int32_t K, int32_t fused, int32_t* out3) {
+  if (!out3 || E < 0) return QVAE_ERR_ARG;
+  const int64_t e = std::max(E, 1), m = std::max<int64_t>(M, 1);
+  int rc = check_linear(e, M, N, K);
+  if (rc) return rc;
+  const int sms = planning_sms();
+  const LinPlan plan = known_plan(e, m, N, K, E > 0, sms);
+  qvae::LinArgs a = {};
+  a.E = static_cast<int>(e);
+  a.Kb = static_cast<int>(ceil_div(K, qvae::kFp8Block));
+  a.NT = plan.NT;
+  uint32_t smem;
+  if ((rc = size_linear(a, plan, fused && quantises_itself(e, m, N, K, E > 0, sms), sms, &smem))) return rc;
+  out3[0] = static_cast<int32_t>(smem);
+  out3[1] = static_cast<int32_t>(a.tmem_cols);
+  out3[2] = (plan.pair ? 2 : 1) * plan.split;
   return QVAE_OK;
 }
 

@@ -40,7 +40,7 @@ EXPORTS = (
     "qvae_fp8_packed_weight_bytes", "qvae_fp8_weight_scale_bytes", "qvae_fp8_quantize_weights",
     "qvae_fp8_code_bytes", "qvae_fp8_scale_bytes", "qvae_fp8_workspace_bytes", "qvae_fp8_quant_act",
     "qvae_linear_fp8", "qvae_linear_fp8_grouped", "qvae_linear_fp8_fused", "qvae_linear_fp8_grouped_fused",
-    "qvae_set_linear_tiling", "qvae_get_linear_tiling",
+    "qvae_set_linear_tiling", "qvae_get_linear_tiling", "qvae_get_linear_footprint",
 )
 
 # qvae_fp8_op: what a linear layer quantises of its rows
@@ -122,6 +122,7 @@ def lib():
             "qvae_linear_fp8_fused": ([i64, i32, i32, i32, p, i64, p, p, p, p, i64, p, sz, p], ctypes.c_int),
             "qvae_set_linear_tiling": ([i32, i32, i32, i32], ctypes.c_int),
             "qvae_get_linear_tiling": ([i32, i64, i32, i32, ctypes.POINTER(i32)], ctypes.c_int),
+            "qvae_get_linear_footprint": ([i32, i64, i32, i32, i32, ctypes.POINTER(i32)], ctypes.c_int),
             "qvae_linear_fp8_grouped_fused": ([i32, i64, i32, i32, i32, p, i64, p, p, p, p, p, i64, p, sz, p],
                                               ctypes.c_int),
         }
@@ -733,3 +734,10 @@ def qvae_get_linear_tiling(E, M, N, K) -> dict:
     out = (ctypes.c_int32 * 3)()
     _check("qvae_get_linear_tiling", lib().qvae_get_linear_tiling(E, M, N, K, out))
     return dict(zip(("NT", "mode", "split"), list(out)))
+
+
+def qvae_get_linear_footprint(E, M, N, K, fused=True) -> dict:
+    """What a CTA of that product takes: bytes of shared memory, TMEM columns, CTAs of its cluster."""
+    out = (ctypes.c_int32 * 3)()
+    _check("qvae_get_linear_footprint", lib().qvae_get_linear_footprint(E, M, N, K, 1 if fused else 0, out))
+    return dict(zip(("smem", "tmem_cols", "cluster"), list(out)))
