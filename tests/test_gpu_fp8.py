@@ -146,6 +146,38 @@ def test_activation_codes_of_silu_mul(q, m, k, extra):
     assert bool(((got[:, :k] - v).abs() <= half * (1 + 2.0 ** -8) + rel * v.abs() + 2.0 ** -149 + lost).all())
 
 
+@pytest.mark.parametrize("up", [1.0, 2.0 ** 40, 2.0 ** 126])
+@pytest.mark.parametrize("gate", [-80.0, -87.0, -87.5, -88.0, -88.5, -89.0, -3.0e38])
+def test_silu_mul_of_gates_whose_exponential_is_next_to_the_largest_number(q, gate, up):
+    # exp(-gate) is an fp32 number down to gate = -88.72: gate / (1 + exp(-gate)) is one, and so is its product with up.
+    # Below it exp(-gate) is infinite in fp32 and the formula gives 0
+    m, k = 3, 300
+    h = torch.empty((m, 2 * k), dtype=torch.bfloat16, device="cuda")
+    h[:, :k] = gate
+    h[:, k:] = rows(m, k, 5).clamp(-3.9, 3.9) * up
+    codes, words = q.fp8_quant_act(h, silu_mul=True)
+    byte = scale_bytes(words, 3)
+    scale = torch.exp2(byte.double() - 127)
+    got = (by_row(codes).view(torch.float8_e4m3fn).double().view(m, -1, 128) * scale[:, :, None]).view(m, -1)
+    if gate <= -89.0:
+        assert (got == 0).all() and (byte == 1).all()
+        return
+    v = ref.silu_mul(h)
+    assert float(v.abs().max()) > 2.0 ** -126
+    s = scale.repeat_interleave(128, 1)[:, :k]
+    half = torch.exp2(torch.floor(torch.log2(torch.clamp(v.abs() / s, min=2.0 ** -6))) - 4) * s
+    rel = (abs(gate) + 4) * 2.0 ** -22                    # as in test_activation_codes_of_silu_mul
+    assert ((got[:, :k] - v).abs() <= half * (1 + 2.0 ** -8) + rel * v.abs() + 2.0 ** -149).all()
+    p = q.fp8_quantize_weights(matrix((64, k), 6))        # quantised by the product: the same codes
+    q.qvae_set_linear_tiling(16, 1, 1)
+    try:
+        one, two = q.linear_fp8_fused(h, p, silu_mul=True), q.linear_fp8(codes, words, p)
+        assert torch.equal(one.view(torch.int16), two.view(torch.int16))
+    finally:
+        q.qvae_set_linear_tiling()
+    assert q.qvae_get_error() == 0
+
+
 @pytest.mark.parametrize("e,n,k", [(1, 1, 1), (1, 128, 128), (2, 130, 200), (1, 1000, 1176), (3, 64, 515), (1, 257, 127)])
 def test_packed_weights_are_exact(q, e, n, k):
     w = matrix((e, n, k), e + n + k)
