@@ -207,3 +207,19 @@ def test_clusters_that_can_share_an_sm_fit_its_tensor_memory():
                 assert a[1] + b[1] <= 512, (a, seen[a], b, seen[b])
     for f in seen:
         assert f[0] <= 232448 and f[1] in (32, 64, 128, 256, 512), (f, seen[f])
+
+
+def test_sizes_beyond_32_bits_are_refused_not_cut():
+    big = 2 ** 32 + 128                                                 # its lower 32 bits are a size in range
+    for bad in ((big, 1, 128), (1, big, 128), (1, 128, big)):
+        assert qvae.qvae_fp8_packed_weight_bytes(*bad) == 0 and qvae.qvae_fp8_weight_scale_bytes(*bad) == 0
+        with pytest.raises(qvae.QvaeError):
+            qvae.qvae_get_linear_tiling(bad[0], 4, bad[1], bad[2])
+        with pytest.raises(qvae.QvaeError):
+            qvae.qvae_get_linear_footprint(bad[0], 4, bad[1], bad[2])
+    assert qvae.qvae_fp8_code_bytes(4, big) == 0 and qvae.qvae_fp8_scale_bytes(4, big) == 0
+    assert qvae.qvae_fp8_workspace_bytes(4, big) == 0
+    for bad in ((2 ** 32 + 16, 0, 0, 0), (0, 2 ** 32 + 1, 0, 0), (0, 0, 2 ** 32 + 2, 0), (0, 0, 0, -2 ** 32 - 1)):
+        with pytest.raises(qvae.QvaeError):
+            qvae.qvae_set_linear_tiling(*bad)
+    qvae.qvae_set_linear_tiling()

@@ -687,6 +687,15 @@ def test_sizes_beyond_32_bits_and_longest(q, m, n, k):
         check_product(out[lo:lo + 40], y, s, k)
 
 
+def test_more_columns_than_32_bits_count_are_refused(q):
+    x = torch.empty((1, 2 ** 32 + 128), dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: q.fp8_quant_act(x), lambda: q.fp8_quant_act(x, silu_mul=True), lambda: q.fp8_quantize_weights(x),
+                 lambda: q.fp8_quantize_weights(x.view(-1, 1))):
+        with pytest.raises(q.QvaeError) as e:
+            call()
+        assert e.value.status == q.QVAE_ERR_SHAPE
+
+
 FIRST_CALL = """
 import torch
 from video_vae_decode_b200 import qvae as q

@@ -463,24 +463,30 @@ class Fp8Weights:
         _buffer(w_scale, torch.uint8, blocks * -(-self.K // 512) * 4, self.device, "w_scale")
 
 
+def _i32(v: int) -> int:
+    """A size as the library takes it.  ctypes drops the bits beyond 32; sizes out of range stay out of range here, for
+    the library to refuse."""
+    return min(max(int(v), -2 ** 31), 2 ** 31 - 1)
+
+
 def qvae_fp8_packed_weight_bytes(E: int, N: int, K: int) -> int:
-    return int(lib().qvae_fp8_packed_weight_bytes(E, N, K))
+    return int(lib().qvae_fp8_packed_weight_bytes(_i32(E), _i32(N), _i32(K)))
 
 
 def qvae_fp8_weight_scale_bytes(E: int, N: int, K: int) -> int:
-    return int(lib().qvae_fp8_weight_scale_bytes(E, N, K))
+    return int(lib().qvae_fp8_weight_scale_bytes(_i32(E), _i32(N), _i32(K)))
 
 
 def qvae_fp8_code_bytes(M: int, K: int) -> int:
-    return int(lib().qvae_fp8_code_bytes(M, K))
+    return int(lib().qvae_fp8_code_bytes(M, _i32(K)))
 
 
 def qvae_fp8_scale_bytes(M: int, K: int) -> int:
-    return int(lib().qvae_fp8_scale_bytes(M, K))
+    return int(lib().qvae_fp8_scale_bytes(M, _i32(K)))
 
 
 def qvae_fp8_workspace_bytes(M: int, K: int) -> int:
-    return int(lib().qvae_fp8_workspace_bytes(M, K))
+    return int(lib().qvae_fp8_workspace_bytes(M, _i32(K)))
 
 
 def _buffer(t: torch.Tensor, dtype: torch.dtype, count: int, device: int, name: str) -> int:
@@ -555,7 +561,7 @@ def fp8_quantize_weights(w: torch.Tensor, stream=None) -> Fp8Weights:
         wq = torch.empty(qvae_fp8_packed_weight_bytes(E, N, K), dtype=torch.uint8, device=w.device)
         ws = torch.empty(qvae_fp8_weight_scale_bytes(E, N, K), dtype=torch.uint8, device=w.device)
         _check("qvae_fp8_quantize_weights",
-               lib().qvae_fp8_quantize_weights(E, N, K, w.data_ptr(), wq.data_ptr(), ws.data_ptr(), handle))
+               lib().qvae_fp8_quantize_weights(_i32(E), _i32(N), _i32(K), w.data_ptr(), wq.data_ptr(), ws.data_ptr(), handle))
         return Fp8Weights(wq, ws, E, N, K)
 
     return _run(device, stream, call)
@@ -580,7 +586,7 @@ def fp8_quant_act(x: torch.Tensor, silu_mul: bool = False, stream=None):
         xq = torch.empty((-(-K // 128), M, 128), dtype=torch.uint8, device=x.device)
         xs = torch.empty((-(-K // 512), M), dtype=torch.int32, device=x.device)
         _check("qvae_fp8_quant_act",
-               lib().qvae_fp8_quant_act(M, K, QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN, x.data_ptr(), ld,
+               lib().qvae_fp8_quant_act(M, _i32(K), QVAE_FP8_SILU_MUL if silu_mul else QVAE_FP8_PLAIN, x.data_ptr(), ld,
                                         xq.data_ptr(), xs.data_ptr(), handle))
         return xq, xs
 
@@ -726,18 +732,18 @@ def qvae_get_conv_tiling(N, T, H, W, Cin, Cout, variant: int = 0) -> dict:
 
 
 def qvae_set_linear_tiling(NT=0, mode=0, split=0, max_ctas=0) -> None:
-    _check("qvae_set_linear_tiling", lib().qvae_set_linear_tiling(NT, mode, split, max_ctas))
+    _check("qvae_set_linear_tiling", lib().qvae_set_linear_tiling(_i32(NT), _i32(mode), _i32(split), _i32(max_ctas)))
 
 
 def qvae_get_linear_tiling(E, M, N, K) -> dict:
     """E = 0: a single layer; else grouped by E experts."""
     out = (ctypes.c_int32 * 3)()
-    _check("qvae_get_linear_tiling", lib().qvae_get_linear_tiling(E, M, N, K, out))
+    _check("qvae_get_linear_tiling", lib().qvae_get_linear_tiling(_i32(E), M, _i32(N), _i32(K), out))
     return dict(zip(("NT", "mode", "split"), list(out)))
 
 
 def qvae_get_linear_footprint(E, M, N, K, fused=True) -> dict:
     """What a CTA of that product takes: bytes of shared memory, TMEM columns, CTAs of its cluster."""
     out = (ctypes.c_int32 * 3)()
-    _check("qvae_get_linear_footprint", lib().qvae_get_linear_footprint(E, M, N, K, 1 if fused else 0, out))
+    _check("qvae_get_linear_footprint", lib().qvae_get_linear_footprint(_i32(E), M, _i32(N), _i32(K), 1 if fused else 0, out))
     return dict(zip(("smem", "tmem_cols", "cluster"), list(out)))
