@@ -4,6 +4,7 @@ refuse (before anything is launched)."""
 import ctypes
 import os
 import sys
+import types
 
 import pytest
 import torch
@@ -223,3 +224,12 @@ def test_sizes_beyond_32_bits_are_refused_not_cut():
         with pytest.raises(qvae.QvaeError):
             qvae.qvae_set_linear_tiling(*bad)
     qvae.qvae_set_linear_tiling()
+
+
+def test_scale_words_of_another_number_of_rows_are_refused():
+    # enough words, but word (g, m) of 6 rows is not where that of 4 rows is (CPU tensors: refused before any launch)
+    weights = types.SimpleNamespace(E=1, N=128, K=600, device=-1)
+    xq = torch.zeros((5, 4, 128), dtype=torch.uint8)
+    for words in (torch.zeros((2, 6), dtype=torch.int32), torch.zeros((2, 3), dtype=torch.int32)):
+        with pytest.raises(ValueError, match="x_scale"):
+            qvae._product(None, "qvae_linear_fp8", xq, words, weights, None, None, None)

@@ -624,7 +624,10 @@ def _product(handle, name, xq, x_scale, weights, bias, out, offsets):
         raise ValueError(f"xq: codes [{-(-K // 128)}, rows, 128] of {K} input channels are needed")
     M = xq.shape[1]
     _buffer(xq, torch.uint8, xq.numel(), device, "xq")
-    _buffer(x_scale, torch.int32, M * -(-K // 512), device, "x_scale")
+    groups = -(-K // 512)
+    _buffer(x_scale, torch.int32, M * groups, device, "x_scale")
+    if groups > 1 and x_scale.dim() > 1 and x_scale.shape[-1] != M:  # (one group: the first M words are the rows')
+        raise ValueError(f"x_scale: scale words [{groups}, {M}] of the {M} rows of xq are needed")
     pb, po = _extras(weights, bias, offsets)
     out, ldo = _out(out, M, N, device)
     if po is None:
