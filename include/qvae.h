@@ -526,7 +526,7 @@ int qvae_set_conv_cta_limit(int32_t max_ctas);
  *   mode      1 = single CTAs, 2 = CTA pairs (cta_group::2)
  *   split     CTAs (or pairs) that share a tile along K, at most 8 CTAs and as
  *             many as there are pairs of 128-channel blocks, and only where
- *             all tiles' CTAs fit the device at a time
+ *             the device holds all tiles' clusters at a time
  *   max_ctas  cap on the CTAs of a launch (split 1)
  * Zero = automatic.  A forced value that a call's sizes do not allow is taken
  * as automatic for that call.

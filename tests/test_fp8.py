@@ -233,3 +233,27 @@ def test_scale_words_of_another_number_of_rows_are_refused():
     for words in (torch.zeros((2, 6), dtype=torch.int32), torch.zeros((2, 3), dtype=torch.int32)):
         with pytest.raises(ValueError, match="x_scale"):
             qvae._product(None, "qvae_linear_fp8", xq, words, weights, None, None, None)
+
+
+# Clusters of 1..8 CTAs that a B200 holds at a time, with one and with two CTAs to an SM, as it answered (without a device
+# the library plans with these).
+HELD = ((148, 74, 45, 33, 26, 22, 15, 15), (296, 148, 93, 71, 56, 45, 37, 33))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="plans for the device that is there")
+def test_the_device_holds_all_clusters_of_a_split():
+    # a split has one tile to a cluster and counts on all of them running at once
+    sizes = [(200, 2048, 8192), (200, 2304, 8192), (87, 384, 11776), (16, 1152, 8192), (1, 2048, 2048), (300, 4096, 4096)]
+    g = torch.Generator().manual_seed(1)
+    for _ in range(3000):
+        sizes.append(tuple(int(2 ** (float(torch.rand(1, generator=g)) * h)) for h in (11, 14, 15)))
+    splits = 0
+    for m, n, k in sizes:
+        t, f = qvae.qvae_get_linear_tiling(0, m, n, k), qvae.qvae_get_linear_footprint(0, m, n, k, False)
+        if t["split"] > 1:
+            splits += 1
+            clusters = -(-m // t["NT"]) * -(-n // (128 * t["mode"]))
+            assert f["cluster"] == t["split"] * t["mode"]
+            two = 2 * (f["smem"] + 1024) <= 228 * 1024
+            assert clusters <= HELD[two][f["cluster"] - 1], (m, n, k, t, f)
+    assert splits > 500

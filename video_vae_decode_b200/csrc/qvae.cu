@@ -596,6 +596,52 @@ struct LinPlan {
   int64_t max_tiles;  // tiles of any offsets
 };
 
+// What a device holds at a time: its SMs, and clusters of 2..8 CTAs with an SM's or half an SM's shared memory each.  A
+// cluster lies inside one GPC, so larger ones leave SMs unused (clusters of 8 reach 120 of a B200's 148).
+struct LinRoom {
+  int sms;
+  int clusters[2][qvae::kLinMaxSplit + 1];  // [CTAs to an SM, less one][CTAs of a cluster]
+};
+
+// As a B200 answered: for planning where there is no device.
+constexpr LinRoom kNoDevice = {148, {{0, 148, 74, 45, 33, 26, 22, 15, 15}, {0, 296, 148, 93, 71, 56, 45, 37, 33}}};
+
+// Shared memory of one of two CTAs on an SM (1 KB of each is the system's).
+constexpr uint32_t kHalfSmem = (kSmemLimit - 1024) / 2;
+
+int device_room(int dev, const LinRoom** out) {
+  static LinRoom rooms[kMaxDevices];
+  static std::atomic<bool> known[kMaxDevices];
+  static std::mutex mutex;
+  if (!known[dev].load(std::memory_order_acquire)) {
+    const std::lock_guard<std::mutex> lock(mutex);
+    LinRoom r = {};
+    const int rc = sm_count(dev, &r.sms);
+    if (rc) return rc;
+    const auto kernel = qvae::linear_room_kernel;
+    QVAE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
+    for (int two = 0; two < 2; ++two) {
+      for (int c = 1; c <= qvae::kLinMaxSplit; ++c) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = c;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * r.sms / c * c);
+        cfg.blockDim = dim3(qvae::kLinThreads);
+        cfg.dynamicSmemBytes = two ? kHalfSmem : kSmemLimit;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        QVAE_CUDA(cudaOccupancyMaxActiveClusters(&r.clusters[two][c], kernel, &cfg));
+      }
+    }
+    rooms[dev] = r;
+    known[dev].store(true, std::memory_order_release);
+  }
+  *out = &rooms[dev];
+  return QVAE_OK;
+}
+
 // Tiles of `nt` rows by one or two output blocks: what the rows give at most (each expert may end in a tile of its own).
 int64_t linear_tiles(int64_t E, int64_t M, int64_t nblk, bool grouped, bool pair, int nt) {
   const int64_t spans = ceil_div(M, nt) + (grouped ? std::min(E, M) - (M > 0 ? 1 : 0) : 0);
@@ -608,8 +654,11 @@ int64_t linear_tiles(int64_t E, int64_t M, int64_t nblk, bool grouped, bool pair
 // 240).  What a launch takes besides was measured on small shapes: about 6000 cycles until the first MMA, an epilogue of
 // 11 cycles a row (22 where half of the warps write it beside the next tile), and for a split along K the larger
 // cluster's start and the sums' way over distributed shared memory (1 x 2048 x 2048: split 2 5.7 us, 4 5.0, 8 5.8).
-// Weights come at 3300 bytes a cycle at most, and 30 to an SM.
-LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms, bool forced = true) {
+// Weights come at 3300 bytes a cycle at most, and 30 to an SM.  A split has one tile to a cluster, so the clusters that
+// the offsets give at most have to fit the device (counted by SMs, 200 x 2048 x 8192 took 16 clusters of 8 where 15 fit,
+// 18.0 us; 32 of 4 take 11.2.  40 random sizes whose tiling differs: 1.6 times faster on average, none slower).
+LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, const LinRoom& room, bool forced = true) {
+  const int sms = room.sms;
   const int64_t nblk = ceil_div(N, qvae::kFp8Block), Kb = ceil_div(K, qvae::kFp8Block);
   const int64_t stages = ceil_div(Kb, qvae::kLinStageBlocks);
   const int64_t busy = grouped ? std::min(E, M) : 1;     // experts that have rows, at most
@@ -634,13 +683,12 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
         if (split > stages || (forced && g_lin_force[2] && split != std::min<int64_t>(g_lin_force[2], stages))) continue;
         // a further CTA that leaves the longest part as it is does not pay
         if (!(forced && g_lin_force[2]) && split > 1 && ceil_div(stages, split) == ceil_div(stages, split - 1)) continue;
-        // one tile to a cluster: what the offsets give at most must fit the device (small single CTAs: twice)
-        const bool twice = !pair && nt <= 32;
-        if (split > 1 && max_tiles * split * ctas > (twice ? 2 : 1) * sms) continue;
+        const bool twice = !pair && nt <= 32;  // (small single CTAs: two to an SM)
+        if (split > 1 && max_tiles > room.clusters[twice][split * ctas]) continue;
         const double part = ceil_div(stages, split) * 4 * qvae::kLinStageBlocks * step;
         const double slots = split > 1 ? max_tiles * split : pair ? sms / 2 : sms;
         const double waves = std::ceil(tiles * split / slots);
-        const double shared = split > 1 && max_tiles * split * ctas > sms ? 2 : 1;  // CTAs on an SM
+        const double shared = split > 1 && max_tiles > room.clusters[0][split * ctas] ? 2 : 1;  // CTAs on an SM
         const double reading = std::min<double>(sms, tiles * split * ctas);         // SMs
         const double epilogue = 1300 + (waves > 1 ? 22 : 11) * n;
         const double steps = waves * part * shared, bytes = weights / std::min(3300.0, 30 * reading);
@@ -654,14 +702,15 @@ LinPlan plan_linear(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, in
       }
     }
   }
-  return best.NT ? best : plan_linear(E, M, N, K, grouped, sms, false);  // nothing that was forced fits
+  return best.NT ? best : plan_linear(E, M, N, K, grouped, room, false);  // nothing that was forced fits
 }
 
 // plan_linear (about 1 us of host time) for sizes that the calling thread used lately is looked up.
-LinPlan known_plan(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms) {
+LinPlan known_plan(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, const LinRoom& room) {
   struct Entry {
     int64_t E = 0, M = 0, N = 0, K = 0;
-    int grouped = -1, sms = 0, force = 0;
+    const LinRoom* room = nullptr;  // the device's
+    int grouped = -1, force = 0;
     LinPlan plan = {};
   };
   constexpr int kEntries = 16;
@@ -669,17 +718,17 @@ LinPlan known_plan(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int
   thread_local int next = 0;
   const int force = g_lin_force[0] | g_lin_force[1] << 8 | g_lin_force[2] << 16;
   for (const Entry& k : known)
-    if (k.M == M && k.N == N && k.K == K && k.E == E && k.grouped == grouped && k.sms == sms && k.force == force)
+    if (k.M == M && k.N == N && k.K == K && k.E == E && k.grouped == grouped && k.room == &room && k.force == force)
       return k.plan;
   Entry& k = known[next];
   next = (next + 1) % kEntries;
-  k.plan = plan_linear(E, M, N, K, grouped, sms);
+  k.plan = plan_linear(E, M, N, K, grouped, room);
   k.E = E;
   k.M = M;
   k.N = N;
   k.K = K;
   k.grouped = grouped;
-  k.sms = sms;
+  k.room = &room;
   k.force = force;
   return k.plan;
 }
@@ -727,9 +776,9 @@ uint32_t linear_smem_besides_ring(int64_t E) {
   return 1024u + qvae::kLinOutWarps * qvae::kLinEpiBuf + qvae::kLinBars + 8u + 4u * static_cast<uint32_t>(3 * E + 1);
 }
 
-// Shared memory of a CTA: all of it, or half where a launch of clusters with one tile each has more CTAs than SMs.
-uint32_t linear_room(const LinPlan& p, int sms) {
-  return p.split > 1 && p.max_tiles * p.split * (p.pair ? 2 : 1) > sms ? (kSmemLimit - 1024) / 2 : kSmemLimit;
+// Shared memory of a CTA: all of it, or half where the device does not hold a launch's clusters, one tile each, otherwise.
+uint32_t linear_smem(const LinPlan& p, const LinRoom& room) {
+  return p.split > 1 && p.max_tiles > room.clusters[0][p.split * (p.pair ? 2 : 1)] ? kHalfSmem : kSmemLimit;
 }
 
 // Shared memory and TMEM of a product's CTAs (a.E, Kb and NT are set).
@@ -739,14 +788,14 @@ uint32_t linear_room(const LinPlan& p, int sms) {
 // (of a pair: more than half), so that two fit and three do not; one of more columns (a split pair of 240 rows) takes
 // so much that no other fits beside it, as pairs without a split and the convolution's pairs do by themselves (170 KB
 // or more wherever they take 512 columns).
-int size_linear(qvae::LinArgs& a, const LinPlan& plan, bool fuse, int sms, uint32_t* smem) {
+int size_linear(qvae::LinArgs& a, const LinPlan& plan, bool fuse, const LinRoom& room, uint32_t* smem) {
   const bool split = plan.split > 1;
   a.box_rows = (a.NT / (plan.pair ? 2 : 1) + qvae::kLinBoxRows - 1) / qvae::kLinBoxRows * qvae::kLinBoxRows;
   a.stage_bytes = qvae::kLinStageBlocks * (qvae::kLinATile + (fuse ? 0u : static_cast<uint32_t>(a.box_rows) * 128u));
   const int blocks = static_cast<int>(ceil_div(ceil_div(a.Kb, qvae::kLinStageBlocks), plan.split)) * qvae::kLinStageBlocks;
   a.codes_bytes = fuse ? static_cast<uint32_t>(blocks) * qvae::kLinFuseRows * qvae::kFp8Block : 0u;
   const uint32_t rest = linear_smem_besides_ring(a.E) + (fuse ? a.codes_bytes + qvae::kLinFuseScales : 0u);
-  a.stages = std::min<int>(qvae::kLinMaxStages, (linear_room(plan, sms) - rest) / a.stage_bytes);
+  a.stages = std::min<int>(qvae::kLinMaxStages, (linear_smem(plan, room) - rest) / a.stage_bytes);
   if (fuse || split) {  // as many as there are; a split tile's sums, NT * 512 bytes, take the ring's place
     const int sums = split ? static_cast<int>(ceil_div(a.NT * qvae::kFp8Block * 4, a.stage_bytes)) : 1;
     a.stages = std::min(a.stages, std::max(blocks / qvae::kLinStageBlocks, sums));
@@ -787,9 +836,10 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
       !aligned2(out) || !aligned4(offsets))
     return QVAE_ERR_ALIGN;
   const bool fuse = rows != nullptr;
-  int dev, sms;
+  int dev;
+  const LinRoom* room;
   if ((rc = current_device(&dev))) return rc;
-  if ((rc = sm_count(dev, &sms))) return rc;
+  if ((rc = device_room(dev, &room))) return rc;
 
   qvae::LinArgs a = {};
   a.E = static_cast<int>(E);
@@ -800,7 +850,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.last_ksteps = static_cast<int>(ceil_div(K - int64_t{a.Kb - 1} * qvae::kFp8Block, 32));
   a.nblk = static_cast<int>(ceil_div(N, qvae::kFp8Block));
   a.kgroups = (a.Kb + 3) / 4;
-  const LinPlan plan = known_plan(E, M, N, K, offsets != nullptr, sms);
+  const LinPlan plan = known_plan(E, M, N, K, offsets != nullptr, *room);
   if (plan.max_tiles > INT32_MAX / 2) return QVAE_ERR_SHAPE;
   const int ctas = (plan.pair ? 2 : 1) * plan.split;  // of a tile
   a.NT = plan.NT;
@@ -812,7 +862,7 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
   a.early = early ? 1 : 0;
   a.tiles_n = plan.pair ? (a.nblk + 1) / 2 : a.nblk;
   uint32_t smem;
-  if ((rc = size_linear(a, plan, fuse, sms, &smem))) return rc;
+  if ((rc = size_linear(a, plan, fuse, *room, &smem))) return rc;
   if (fuse) {
     a.x = static_cast<const __nv_bfloat16*>(rows->x);
     a.ldx = rows->ldx;
@@ -853,12 +903,12 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
     QVAE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit));
     attr_set = true;
   }
-  int grid = sms;
+  int grid = room->sms;
   if (fuse || plan.split > 1) {
     grid = static_cast<int>(plan.max_tiles) * ctas;  // one tile each
   } else {
     if (plan.pair) {
-      if ((rc = max_pairs(kernel, qvae::kLinThreads, sms, &g_lin_max_clusters[dev]))) return rc;
+      if ((rc = max_pairs(kernel, qvae::kLinThreads, room->sms, &g_lin_max_clusters[dev]))) return rc;
       grid = 2 * g_lin_max_clusters[dev];
     }
     if (const int cap = g_lin_force[3]) grid = std::min(grid, cap);
@@ -869,24 +919,25 @@ int launch_linear(int64_t E, int64_t M, int64_t N, int64_t K, const uint8_t* xq,
 }
 
 // Whether the product quantises its rows itself: few rows, one tile to a CTA, and a CTA's part of K in shared memory.
-bool quantises_itself(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, int sms) {
-  const LinPlan plan = known_plan(E, M, N, K, grouped, sms);
+bool quantises_itself(int64_t E, int64_t M, int64_t N, int64_t K, bool grouped, const LinRoom& room) {
+  const LinPlan plan = known_plan(E, M, N, K, grouped, room);
   const int64_t blocks =
       ceil_div(ceil_div(ceil_div(K, qvae::kFp8Block), qvae::kLinStageBlocks), plan.split) * qvae::kLinStageBlocks;
   // two stages of weights beside the codes
   const int64_t smem = linear_smem_besides_ring(E) + blocks * qvae::kLinFuseRows * qvae::kFp8Block + qvae::kLinFuseScales +
                        2 * qvae::kLinStageBlocks * qvae::kLinATile;
-  return !plan.pair && plan.NT <= qvae::kLinFuseRows && plan.max_tiles * plan.split <= (plan.split > 1 ? 2 : 1) * sms &&
+  return !plan.pair && plan.NT <= qvae::kLinFuseRows && (plan.split > 1 || plan.max_tiles <= room.sms) &&
          blocks <= qvae::kLinFuseBlocks && std::min<int64_t>(M, plan.NT) * blocks <= qvae::kLinFuseItems &&
-         smem <= linear_room(plan, sms);
+         smem <= linear_smem(plan, room);
 }
 
-// SMs of the current device, or a B200's where there is none.
-int planning_sms() {
-  int sms = 148, dev;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) sm_count(dev, &sms);
+// The current device's room, or a B200's where there is none.
+const LinRoom& planning_room() {
+  int dev;
+  const LinRoom* room = &kNoDevice;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || device_room(dev, &room)) room = &kNoDevice;
   cudaGetLastError();
-  return sms;
+  return *room;
 }
 
 // The layer from bf16 rows: one launch for few rows; else the quantiser into the workspace, then the product.
@@ -909,10 +960,11 @@ int launch_linear_fused(int64_t E, int64_t M, int64_t N, int64_t K, int op, cons
   if (ldx > INT64_MAX / 2 / M) return QVAE_ERR_SHAPE;
   if (!aligned2(x)) return QVAE_ERR_ALIGN;
   if (x == out) return QVAE_ERR_ARG;  // in one launch a CTA's outputs would meet rows that others still read
-  int dev, sms;
+  int dev;
+  const LinRoom* room;
   if ((rc = current_device(&dev))) return rc;
-  if ((rc = sm_count(dev, &sms))) return rc;
-  if (quantises_itself(E, M, N, K, offsets != nullptr, sms))
+  if ((rc = device_room(dev, &room))) return rc;
+  if (quantises_itself(E, M, N, K, offsets != nullptr, *room))
     return launch_linear(E, M, N, K, nullptr, nullptr, offsets, wq, w_scale, bias, out, ldo, stream, false, &rows);
   uint8_t* const xq = static_cast<uint8_t*>(workspace);
   uint32_t* const x_scale = reinterpret_cast<uint32_t*>(xq + round256(qvae_fp8_code_bytes(M, K)));
@@ -1434,7 +1486,7 @@ int qvae_get_linear_tiling(int32_t E, int64_t M, int32_t N, int32_t K, int32_t* 
   const int rc = check_linear(std::max(E, 1), M, N, K);
   if (rc) return rc;
   if (E < 0) return QVAE_ERR_ARG;
-  const LinPlan plan = plan_linear(std::max(E, 1), std::max<int64_t>(M, 1), N, K, E > 0, planning_sms());
+  const LinPlan plan = plan_linear(std::max(E, 1), std::max<int64_t>(M, 1), N, K, E > 0, planning_room());
   out3[0] = plan.NT;
   out3[1] = plan.pair ? 2 : 1;
   out3[2] = plan.split;
@@ -1446,14 +1498,14 @@ int qvae_get_linear_footprint(int32_t E, int64_t M, int32_t N, int32_t K, int32_
   const int64_t e = std::max(E, 1), m = std::max<int64_t>(M, 1);
   int rc = check_linear(e, M, N, K);
   if (rc) return rc;
-  const int sms = planning_sms();
-  const LinPlan plan = known_plan(e, m, N, K, E > 0, sms);
+  const LinRoom& room = planning_room();
+  const LinPlan plan = known_plan(e, m, N, K, E > 0, room);
   qvae::LinArgs a = {};
   a.E = static_cast<int>(e);
   a.Kb = static_cast<int>(ceil_div(K, qvae::kFp8Block));
   a.NT = plan.NT;
   uint32_t smem;
-  if ((rc = size_linear(a, plan, fused && quantises_itself(e, m, N, K, E > 0, sms), sms, &smem))) return rc;
+  if ((rc = size_linear(a, plan, fused && quantises_itself(e, m, N, K, E > 0, room), room, &smem))) return rc;
   out3[0] = static_cast<int32_t>(smem);
   out3[1] = static_cast<int32_t>(a.tmem_cols);
   out3[2] = (plan.pair ? 2 : 1) * plan.split;
