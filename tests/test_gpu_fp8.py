@@ -720,3 +720,156 @@ def test_first_call_of_a_process_inside_a_capture(q):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     res = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert res.returncode == 0 and res.stdout.strip() == "ok", res.stderr[-2000:]
+
+
+# -------------------------------------------- exact sums, far offsets, company
+
+@pytest.mark.parametrize("m", [1, 3, 20, 130])
+@pytest.mark.parametrize("k", [1 << 20, (1 << 20) - 77, 300001])
+def test_every_block_of_a_long_row_counts_once(q, m, k):
+    # One channel of each 128-block is not zero, and its products with output n are 2^0 .. 2^7 of eight blocks of n's:
+    # the sum 255 * 2^r of row r is exact in fp32 and in bf16, so a block that is missing, counted twice or scaled by
+    # another's byte shows.  128 outputs have 1024 blocks in a pass; the passes go through all of them.
+    n, kb = 128, -(-k // 128)
+    b = torch.arange(kb)
+    last = torch.clamp(k - b * 128, max=128)
+    at = (b * 128 + (b * 37 + 5) % last).cuda()             # the channel of each block
+    a = ((b * 7) % 21 - 10).cuda()                          # its power of two: the scales differ from block to block
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device="cuda")
+    r = (torch.arange(m) % 5).cuda()
+    x[:, at] = torch.exp2((a[None, :] + r[:, None]).float()).to(torch.bfloat16)
+    assert torch.equal((x != 0).sum(1), torch.full((m,), kb, device="cuda"))
+    codes = q.fp8_quant_act(x)
+    for first in range(0, kb, 8 * n):
+        mine = b[first:first + 8 * n].cuda()
+        w = torch.zeros((n, k), dtype=torch.bfloat16, device="cuda")
+        # blocks next to one another belong to different outputs: those at the edge of a part of K too
+        out, bit = (mine - first) % n, (mine - first) // n
+        w[out, at[mine]] = torch.exp2((bit - a[mine]).float()).to(torch.bfloat16)
+        want = torch.zeros(n, dtype=torch.float64, device="cuda").index_add_(0, out, torch.exp2(bit.double()))
+        want = torch.exp2(r.double())[:, None] * want
+        p = q.fp8_quantize_weights(w)
+        assert torch.equal(q.linear_fp8(*codes, p).double(), want)
+        assert torch.equal(q.linear_fp8_fused(x, p).double(), want)
+
+
+def check_sharp(out, y, s, K):
+    """check_product where its tolerance is well below the outputs."""
+    assert float(ref.tolerance(y, s, K).median()) < 0.05 * float(y.abs().median())
+    check_product(out, y, s, K)
+
+
+def test_codes_beyond_32_bits(q):
+    m, n, k = 300000, 40, 8192                              # 2.46e9 codes and values of x
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((m, k), generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = matrix((n, k), 2)
+    out = q.linear_fp8_fused(x, q.fp8_quantize_weights(w))
+    for lo in (0, m // 2, (1 << 31) // k - 20, m - 40):     # also around the 2^31st value
+        y, s = ref.linear(ref.act_values(x[lo:lo + 40]), ref.weight_values(w))
+        check_sharp(out[lo:lo + 40], y, s, k)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("m", [9, 50000])
+def test_rows_far_apart(q, m, silu):
+    # rows whose first values are more than 2^32 values behind the first row's, on 16 bytes and not
+    n, k, ldx = 72, 264, (1 << 29) + 9 if m == 9 else 100008
+    buf = torch.empty((m - 1) * ldx + 2 * k, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(buf, (m, (2 if silu else 1) * k), (ldx, 1))
+    dense = rows(m, x.shape[1], 3)
+    x.copy_(dense)
+    p = q.fp8_quantize_weights(matrix((n, k), 4))
+    out = q.linear_fp8_fused(x, p, silu_mul=silu)
+    assert torch.equal(out, q.linear_fp8_fused(dense, p, silu_mul=silu))
+    if not silu:
+        y, s = ref.linear(ref.act_values(dense[-9:]), ref.weight_values(matrix((n, k), 4)))
+        check_sharp(out[-9:], y, s, k)
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 2, 1], [16, 1, 0, 15], [100, 0, 301, 20]])
+def test_second_product_of_a_feed_forward_is_that_of_its_codes(q, counts):
+    e, d, inner = len(counts), 320, 200
+    o = spans(counts)
+    x, w1, w2 = rows(o[-1], d, 1), matrix((e, 2 * inner, d), 2), matrix((e, d, inner), 3)
+    offsets = torch.tensor(o, dtype=torch.int32, device="cuda")
+    h, out = feed_forward(q, x, offsets, q.fp8_quantize_weights(w1), q.fp8_quantize_weights(w2))
+    codes, words = q.fp8_quant_act(h, silu_mul=True)        # tested by itself
+    byte = scale_bytes(words, -(-inner // 128)).double()
+    v = (by_row(codes).view(torch.float8_e4m3fn).double().view(o[-1], -1, 128) * torch.exp2(byte - 127)[:, :, None])
+    v = v.view(o[-1], -1)[:, :inner]
+    for i in range(e):
+        lo, hi = o[i], o[i + 1]
+        if hi > lo:
+            y, s = ref.linear(v[lo:hi], ref.weight_values(w2[i]))
+            check_sharp(out[lo:hi], y, s, inner)
+
+
+def company(q):
+    """Calls of every kind of launch: what each writes, from inputs of its own."""
+    from video_vae_decode_b200 import synth
+
+    def linear(m, n, k, want, silu=False):
+        x, p = rows(m, (2 if silu else 1) * k, m), q.fp8_quantize_weights(matrix((n, k), n))
+        got = q.qvae_get_linear_tiling(0, m, n, k)
+        assert (got["mode"], got["split"] > 1) == want, got
+        return lambda: q.linear_fp8_fused(x, p, silu_mul=silu)
+
+    t = synth.draw_custom(synth.LayerShape(128, 128, 96, 96, T=2), seed=3, outliers=True)
+    cx, cb = t.x.cuda(), t.bias.cuda()
+    packed, s_w = q.quantize_weights(t.w.cuda())
+
+    def conv():
+        xq, s_a = q.act_absmax_quant(cx)
+        return q.causal_conv3d_w8a8(xq, s_a, packed, s_w, cb, 128)
+
+    ge = rows(64, 1024, 2)
+    gp, go = q.fp8_quantize_weights(matrix((8, 512, 1024), 3)), torch.tensor([0, 3, 3, 20, 21, 40, 50, 63, 64], dtype=torch.int32, device="cuda")
+    return [linear(16, 8192, 4096, (1, True)), linear(1, 4096, 8192, (1, True), True), linear(363, 1964, 11014, (2, True)),
+            linear(300, 4096, 4096, (2, False)), linear(16, 1152, 8192, (1, True)), linear(77, 1000, 1176, (1, False)),
+            lambda: q.linear_fp8_grouped_fused(ge, go, gp), conv]
+
+
+def test_every_kind_of_launch_beside_every_other(q):
+    # clusters, pairs and convolutions that wait for their SMs, their TMEM and one another, on four streams
+    jobs = company(q)
+    want = [job() for job in jobs]
+    torch.cuda.synchronize()
+    g = torch.Generator().manual_seed(7)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for _ in range(12):
+        for s in streams:
+            i = int(torch.randint(0, len(jobs), (1,), generator=g))
+            with torch.cuda.stream(s):
+                got.append((i, jobs[i]()))
+    torch.cuda.synchronize()
+    for i, out in got:
+        assert torch.equal(out, want[i]), i
+
+
+def test_calls_of_several_threads(q):
+    import threading
+
+    jobs = company(q)
+    want = [job() for job in jobs]
+    torch.cuda.synchronize()
+    wrong, done = [], []
+
+    def work(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                outs = [((k + r) % len(jobs), jobs[(k + r) % len(jobs)]()) for r in range(16)]
+                torch.cuda.current_stream().synchronize()
+                wrong.extend(i for i, out in outs if not torch.equal(out, want[i]))
+            done.append(k)
+        except Exception as e:  # (an assertion of the main thread's shows it)
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    torch.cuda.synchronize()
+    assert not wrong and len(done) == 4, wrong
