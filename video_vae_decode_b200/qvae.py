@@ -444,7 +444,9 @@ def qvae_decode_layers(layers, workspace: torch.Tensor, stream=None) -> None:
 #
 # Tensors on another device than the current one run on their own device (its
 # current stream by default).  What a wrapper allocates is allocated on the
-# stream that the call runs on.
+# stream that the call runs on.  Inference only, as everywhere in this library:
+# no call records a gradient, and the outputs of tensors that require one do
+# not.
 
 class Fp8Weights:
     """Packed e4m3 weights of E matrices [N, K] (qvae_fp8_quantize_weights): wq, uint8 of
@@ -551,7 +553,8 @@ def _run(device: int, stream, call, *args):
 
 
 def fp8_quantize_weights(w: torch.Tensor, stream=None) -> Fp8Weights:
-    """Quantise and pack bf16 weights [N, K] or, one matrix to an expert, [E, N, K]."""
+    """Quantise and pack bf16 weights [N, K] or, one matrix to an expert, [E, N, K]: their values as they are now; later
+    changes of w, an optimizer's too, do not reach the packed ones."""
     device = _device(w, "w")
     if w.dtype != torch.bfloat16 or w.dim() not in (2, 3) or not w.is_contiguous():
         raise ValueError("w: contiguous bf16 weights [N, K] or [E, N, K] are needed")
@@ -644,7 +647,7 @@ def _product(handle, name, xq, x_scale, weights, bias, out, offsets):
 
 def linear_fp8(xq: torch.Tensor, x_scale: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """bf16 [M, N] of quantised rows (fp8_quant_act) and one weight matrix."""
+    """bf16 [M, N] of quantised rows (fp8_quant_act) and one weight matrix.  Records no gradient."""
     return _run(weights.device, stream, _product, "qvae_linear_fp8", xq, x_scale, weights, bias, out, None)
 
 
@@ -684,7 +687,7 @@ def _fused(handle, name, x, weights, bias, silu_mul, out, workspace, offsets):
 def linear_fp8_fused(x: torch.Tensor, weights: Fp8Weights, bias: Optional[torch.Tensor] = None, silu_mul: bool = False,
                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
-    """bf16 [M, N] of bf16 rows x [M, K] (silu_mul: [M, 2 K] = [gate | up]), quantised on the way."""
+    """bf16 [M, N] of bf16 rows x [M, K] (silu_mul: [M, 2 K] = [gate | up]), quantised on the way.  Records no gradient."""
     return _run(weights.device, stream, _fused, "qvae_linear_fp8_fused", x, weights, bias, silu_mul, out, workspace,
                 None)
 
@@ -693,7 +696,7 @@ def linear_fp8_grouped_fused(x: torch.Tensor, offsets: torch.Tensor, weights: Fp
                              bias: Optional[torch.Tensor] = None, silu_mul: bool = False,
                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                              stream=None) -> torch.Tensor:
-    """linear_fp8_grouped of bf16 rows, quantised on the way."""
+    """linear_fp8_grouped of bf16 rows, quantised on the way.  Records no gradient."""
     if offsets is None:
         raise ValueError("offsets: an int32 tensor is needed")
     return _run(weights.device, stream, _fused, "qvae_linear_fp8_grouped_fused", x, weights, bias, silu_mul, out,
