@@ -509,9 +509,11 @@ struct LinTiles {
 // of four 128-channel blocks into TMEM (every lane quarter holds a copy: warp %
 // 4 is the quarter a warp can reach), warps 6-9 write the outputs.
 //
-// Measured, product alone: 8192 x 8192 x 4096 in 209-215 us (2.6 PFLOP/s; tensor
-// pipe 89 % active, at the power cap in a loop), 16384 rows over 64 experts of
-// 2048 x 2048 in 87 us, 64 rows over 24 of 32 such experts in 20 us (5.0 TB/s).
+// Measured, product alone (without its quantiser): 8192 x 8192 x 4096 in 197 us
+// in short bursts (2.8 PFLOP/s; tensor pipe 89 % active) and 228 us in a loop of
+// seconds, at the power cap and 1.2 GHz; 16384 rows over 64 experts of
+// 2048 x 2048 in 81 and 97 us; 64 rows over 24 of 32 such experts in 20.5 us
+// (4.9 TB/s).
 //
 // kPair: a CTA pair runs the tensor cores' cta_group::2 path.  A tile is then
 // 256 output channels; each CTA loads its own 128 rows of weights and half of
