@@ -809,11 +809,13 @@ def company(q):
     """Calls of every kind of launch: what each writes, from inputs of its own."""
     from video_vae_decode_b200 import synth
 
-    def linear(m, n, k, want, silu=False):
+    def linear(m, n, k, silu=False):
         x, p = rows(m, (2 if silu else 1) * k, m), q.fp8_quantize_weights(matrix((n, k), n))
-        got = q.qvae_get_linear_tiling(0, m, n, k)
-        assert (got["mode"], got["split"] > 1) == want, got
         return lambda: q.linear_fp8_fused(x, p, silu_mul=silu)
+
+    def kind(size):
+        t = q.qvae_get_linear_tiling(0, *size)
+        return t["mode"], t["split"] > 1
 
     t = synth.draw_custom(synth.LayerShape(128, 128, 96, 96, T=2), seed=3, outliers=True)
     cx, cb = t.x.cuda(), t.bias.cuda()
@@ -825,9 +827,11 @@ def company(q):
 
     ge = rows(64, 1024, 2)
     gp, go = q.fp8_quantize_weights(matrix((8, 512, 1024), 3)), torch.tensor([0, 3, 3, 20, 21, 40, 50, 63, 64], dtype=torch.int32, device="cuda")
-    return [linear(16, 8192, 4096, (1, True)), linear(1, 4096, 8192, (1, True), True), linear(363, 1964, 11014, (2, True)),
-            linear(300, 4096, 4096, (2, False)), linear(16, 1152, 8192, (1, True)), linear(77, 1000, 1176, (1, False)),
-            lambda: q.linear_fp8_grouped_fused(ge, go, gp), conv]
+    # how many clusters a device holds decides which sizes are split over pairs
+    sizes = [(363, 1964, 11014), (200, 2304, 8192), (469, 1500, 6706), (349, 720, 16341), (16, 8192, 4096), (300, 4096, 4096),
+             (16, 1152, 8192), (77, 1000, 1176)]
+    assert {(1, True), (1, False), (2, False)} <= {kind(s) for s in sizes}
+    return [linear(*s) for s in sizes] + [linear(1, 4096, 8192, True), lambda: q.linear_fp8_grouped_fused(ge, go, gp), conv]
 
 
 def test_every_kind_of_launch_beside_every_other(q):

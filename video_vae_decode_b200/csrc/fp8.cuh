@@ -130,7 +130,7 @@ __device__ __forceinline__ uint32_t abs_max_bf16x8(const uint4& w) {
 // an exponential with subnormal results takes.)
 __device__ __forceinline__ float silu_mul(float g, float u) {
   float t, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(g, -1.44269504f, -2.0f)));  // log2(e)
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(g, -1.44269504f, -2.0f)));  // 2^(-g log2(e) - 2)
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t + 0.25f));
   return 0.25f * g * r * u;
 }
